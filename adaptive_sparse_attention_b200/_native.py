@@ -10,7 +10,7 @@ import os
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libentmax_attn.so")
 
-OK, EINVAL, EALIGN, ECUDA, ETIMEOUT, ENOMEM = 0, 1, 2, 3, 4, 5
+OK, EINVAL, EALIGN, ECUDA, ETIMEOUT, ENOMEM, ERANGE = 0, 1, 2, 3, 4, 5, 6
 FP32, BF16 = 0, 1
 FLAG_CUDA_CORES = 1
 FLAG_ALL_FALLBACK = 2
@@ -21,7 +21,7 @@ FLAG_OUT_FP32 = 32  # fp32 out for bf16 inputs (ENTMAX_ATTN_FLAG_OUT_FP32)
 NOALLOC_SCRATCH_BYTES = 16 << 20  # ENTMAX_ATTN_NOALLOC_SCRATCH_BYTES
 
 _c_int, _c_float, _c_size_t, _vp = ctypes.c_int, ctypes.c_float, ctypes.c_size_t, ctypes.c_void_p
-_c_uint = ctypes.c_uint
+_c_uint, _ll = ctypes.c_uint, ctypes.c_longlong
 
 # name -> (restype, argtypes); kept in the order of include/entmax_attn.h
 SIGNATURES = {
@@ -54,6 +54,15 @@ SIGNATURES = {
     "entmax_attn_route_chunks": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int,
                                           _c_int, _c_int, _c_float, _c_int, _c_int, _c_int,
                                           _c_float, _c_int, _vp]),
+    "entmax_attn_page_tables": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _ll, _c_int, _c_int,
+                                         _c_int, _vp, _c_int, _c_int, _vp, _vp, _vp, _vp]),
+    "entmax_attn_paged_append": (_c_int, [_vp, _vp, _ll, _ll, _ll, _vp, _vp, _ll, _ll, _ll,
+                                          _c_int, _c_int, _vp, _c_int, _c_int, _c_int, _c_int,
+                                          _c_int, _vp]),
+    "entmax_attn_decode_workspace_bytes": (_c_size_t, [_c_int, _c_int, _c_int, _c_int]),
+    "entmax_attn_decode": (_c_int, [_vp, _ll, _ll, _vp, _vp, _ll, _ll, _ll, _c_int, _c_int, _vp,
+                                    _ll, _c_int, _vp, _vp, _vp, _vp, _c_size_t, _c_int, _c_int,
+                                    _c_int, _c_int, _c_int, _c_float, _c_int, _c_int, _vp]),
     "entmax_attn_status": (_c_int, [_vp]),
     "entmax_attn_release_workspaces": (None, []),
     "entmax_attn_fwd_noalloc": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int,

@@ -2,10 +2,12 @@
 // and the launch sequence of the two passes.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <utility>
@@ -469,6 +471,51 @@ int entmax_attn_bwd(const void* q, const void* k, const void* v, const void* dou
 
 namespace {
 
+// Checks of a paged cache (device pointers, strides in elements).
+int check_cache(const void* k, const void* v, long long page_stride, long long head_stride,
+                long long slot_stride, int num_pages, int page_size, int d, int dtype) {
+  if (!k || !v || num_pages < 1 || page_size < 1 || (d != 64 && d != 128) ||
+      (dtype != ENTMAX_ATTN_FP32 && dtype != ENTMAX_ATTN_BF16) || page_stride < d ||
+      head_stride < d || slot_stride < d)
+    return ENTMAX_ATTN_EINVAL;
+  const long long esz = dtype == ENTMAX_ATTN_FP32 ? 4 : 2;
+  if ((page_stride * esz) % 16 || (head_stride * esz) % 16 || (slot_stride * esz) % 16)
+    return ENTMAX_ATTN_EINVAL;
+  return aligned16(k) && aligned16(v) ? ENTMAX_ATTN_OK : ENTMAX_ATTN_EALIGN;
+}
+
+// Sizes of a decode call and its workspace: [prefix sums | parts | candidates], each section
+// 256-byte aligned.  A candidate list has a place for every key, so no list overflows whatever the
+// scores; only the candidates (z > running max - 1) are written.  Returns the bytes, 0 on bad
+// sizes.
+size_t decode_layout(void* base, int B, int Hq, int Hkv, int max_len, ea::DecodeProblem* P) {
+  if (B < 1 || B > ea::kMaxRequests || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 1)
+    return 0;
+  P->B = B;
+  P->Hq = Hq;
+  P->Hkv = Hkv;
+  P->G = Hq / Hkv;
+  P->max_len = max_len;
+  P->heads_per_block = P->G <= 8 ? 8 : 16;
+  P->head_blocks = (P->G + P->heads_per_block - 1) / P->heads_per_block;
+  P->score_warps = ea::kDecodeScoreWarps;
+  P->cand_stride = (static_cast<int64_t>(max_len) + 15) / 16 * 16;
+  const int64_t groups = static_cast<int64_t>(B) * Hkv * P->head_blocks;
+  // unit counts and their sum over the batch are 32-bit on the device
+  if (static_cast<int64_t>(B) * (P->cand_stride / 16) >= (int64_t(1) << 31)) return 0;
+  if (Hq > (1 << 24)) return 0;
+  char* p = static_cast<char*>(base);
+  size_t off = 0;
+  P->pre = reinterpret_cast<int32_t*>(p + off);
+  off += align256(sizeof(int32_t) * (static_cast<size_t>(B) + 1));
+  P->parts = reinterpret_cast<int2*>(p + off);
+  off += align256(sizeof(int2) * static_cast<size_t>(P->score_warps + groups) *
+                  P->heads_per_block);
+  P->cand = reinterpret_cast<int2*>(p + off);
+  off += align256(sizeof(int2) * static_cast<size_t>(B) * Hq * P->cand_stride);
+  return off;
+}
+
 // Both passes on the library's cached workspace of (device, stream); flags as the two-pass form.
 int fwd_cached(const void* q, const void* k, const void* v, void* out, float* tau,
                uint32_t* block_mask, int B, int Hq, int Hkv, int T, int d, float alpha,
@@ -574,6 +621,147 @@ int entmax_attn_route_chunks(const void* q, const void* summaries, float* pi, fl
   return ENTMAX_ATTN_OK;
 }
 
+int entmax_attn_page_tables(const int32_t* lens, const int32_t* new_lens,
+                            const int32_t* free_pages, int n_free, const int32_t* free_start,
+                            int32_t* block_tables, long long table_stride, int W, int B,
+                            int page_size, int64_t* slots, int n_new, int padded,
+                            int32_t* lens_out, int32_t* cu_new, int32_t* free_next,
+                            cudaStream_t stream) {
+  if (!lens || !new_lens || (!free_pages && n_free != 0) || !free_start || !block_tables ||
+      !slots || !lens_out || !cu_new || !free_next || n_free < 0 || W < 1 || B < 1 ||
+      B > ea::kMaxRequests || table_stride < W || page_size < 1 || n_new < 1 ||
+      (padded != 0 && padded != 1) || lens_out == lens || lens_out == new_lens ||
+      free_next == free_start || static_cast<int64_t>(B) * W >= (int64_t(1) << 31))
+    return ENTMAX_ATTN_EINVAL;
+  for (const void* p : {static_cast<const void*>(lens), static_cast<const void*>(new_lens),
+                        static_cast<const void*>(free_pages),
+                        static_cast<const void*>(free_start),
+                        static_cast<const void*>(block_tables),
+                        static_cast<const void*>(lens_out), static_cast<const void*>(cu_new),
+                        static_cast<const void*>(free_next)})
+    if (reinterpret_cast<uintptr_t>(p) & 3u) return ENTMAX_ATTN_EALIGN;
+  if (reinterpret_cast<uintptr_t>(slots) & 7u) return ENTMAX_ATTN_EALIGN;
+  ea::PageTables P = {};
+  P.lens = lens;
+  P.new_lens = new_lens;
+  P.free_pages = free_pages;
+  P.free_start = free_start;
+  P.tables = block_tables;
+  P.table_stride = table_stride;
+  P.table_tokens = std::min(static_cast<int64_t>(W) * page_size, (int64_t(1) << 31) - 1);
+  P.slots = slots;
+  P.lens_out = lens_out;
+  P.cu_new = cu_new;
+  P.free_next = free_next;
+  P.n_free = n_free;
+  P.B = B;
+  P.page_size = page_size;
+  P.n_new = n_new;
+  P.padded = padded;
+  const cudaError_t e = ea::launch_page_tables(P, stream);
+  return e == cudaSuccess ? ENTMAX_ATTN_OK : cuda_fail(e);
+}
+
+int entmax_attn_paged_append(const void* k, const void* v, long long stride_b, long long stride_h,
+                             long long stride_t, void* k_cache, void* v_cache,
+                             long long page_stride, long long head_stride, long long slot_stride,
+                             int num_pages, int page_size, const int64_t* slots, int B, int Hkv,
+                             int T, int d, int dtype, cudaStream_t stream) {
+  if (!k || !v || !slots || B < 1 || Hkv < 1 || T < 1 ||
+      static_cast<int64_t>(B) * T >= (int64_t(1) << 31) || stride_b < 0 || stride_h < 0 ||
+      stride_t < 0)
+    return ENTMAX_ATTN_EINVAL;
+  int rc = check_cache(k_cache, v_cache, page_stride, head_stride, slot_stride, num_pages,
+                       page_size, d, dtype);
+  if (rc != ENTMAX_ATTN_OK) return rc;
+  const long long esz = dtype == ENTMAX_ATTN_FP32 ? 4 : 2;
+  if ((stride_b * esz) % 16 || (stride_h * esz) % 16 || (stride_t * esz) % 16)
+    return ENTMAX_ATTN_EINVAL;
+  if (!aligned16(k) || !aligned16(v) || (reinterpret_cast<uintptr_t>(slots) & 7u))
+    return ENTMAX_ATTN_EALIGN;
+  ea::PagedAppend P = {};
+  int err = ENTMAX_ATTN_OK;
+  P.status = status_ptr(&err);
+  if (!P.status) return err;
+  P.k = k;
+  P.v = v;
+  P.k_cache = k_cache;
+  P.v_cache = v_cache;
+  P.slots = slots;
+  P.stride_b = stride_b * esz;
+  P.stride_h = stride_h * esz;
+  P.stride_t = stride_t * esz;
+  P.page_stride = page_stride * esz;
+  P.head_stride = head_stride * esz;
+  P.slot_stride = slot_stride * esz;
+  P.n_slots = static_cast<int64_t>(num_pages) * page_size;
+  P.n_tokens = B * T;
+  P.T = T;
+  P.Hkv = Hkv;
+  P.page_size = page_size;
+  const cudaError_t e = ea::launch_paged_append(P, static_cast<int>(d * esz), stream);
+  return e == cudaSuccess ? ENTMAX_ATTN_OK : cuda_fail(e);
+}
+
+size_t entmax_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int max_len) {
+  ea::DecodeProblem P = {};
+  return decode_layout(nullptr, B, Hq, Hkv, max_len, &P);
+}
+
+int entmax_attn_decode(const void* q, long long q_stride_b, long long q_stride_h,
+                       const void* k_cache, const void* v_cache, long long page_stride,
+                       long long head_stride, long long slot_stride, int num_pages, int page_size,
+                       const int32_t* block_tables, long long table_stride, int W,
+                       const int32_t* seq_lens, void* out, float* tau, void* workspace,
+                       size_t workspace_bytes, int B, int Hq, int Hkv, int max_len, int d,
+                       float alpha, int n_iter, int dtype, cudaStream_t stream) {
+  if (!q || !block_tables || !seq_lens || !out || !tau || !workspace || W < 1 ||
+      table_stride < W || q_stride_b < 0 || q_stride_h < 0 || !std::isfinite(alpha) ||
+      !(alpha > 1.f) || n_iter < 1 || n_iter > 1000)
+    return ENTMAX_ATTN_EINVAL;
+  int rc = check_cache(k_cache, v_cache, page_stride, head_stride, slot_stride, num_pages,
+                       page_size, d, dtype);
+  if (rc != ENTMAX_ATTN_OK) return rc;
+  if (max_len > static_cast<int64_t>(W) * page_size) return ENTMAX_ATTN_EINVAL;
+  const long long esz = dtype == ENTMAX_ATTN_FP32 ? 4 : 2;
+  if ((q_stride_b * esz) % 16 || (q_stride_h * esz) % 16) return ENTMAX_ATTN_EINVAL;
+  const double a = static_cast<double>(alpha);
+  const float beta = static_cast<float>(1.0 / (a - 1.0));
+  if (!std::isfinite(beta)) return ENTMAX_ATTN_EINVAL;
+  ea::DecodeProblem P = {};
+  const size_t need = decode_layout(workspace, B, Hq, Hkv, max_len, &P);
+  if (need == 0) return ENTMAX_ATTN_EINVAL;
+  if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
+      (reinterpret_cast<uintptr_t>(seq_lens) & 3u) || (reinterpret_cast<uintptr_t>(tau) & 3u) ||
+      (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return ENTMAX_ATTN_EALIGN;
+  if (workspace_bytes < need) return ENTMAX_ATTN_ENOMEM;
+  int err = ENTMAX_ATTN_OK;
+  P.status = status_ptr(&err);
+  if (!P.status) return err;
+  P.q = q;
+  P.k = k_cache;
+  P.v = v_cache;
+  P.tables = block_tables;
+  P.lens = seq_lens;
+  P.out = out;
+  P.tau = tau;
+  P.q_stride_b = q_stride_b;
+  P.q_stride_h = q_stride_h;
+  P.page_stride = page_stride;
+  P.head_stride = head_stride;
+  P.slot_stride = slot_stride;
+  P.table_stride = table_stride;
+  P.num_pages = num_pages;
+  P.page_size = page_size;
+  P.n_iter = n_iter;
+  P.alpha = alpha;
+  P.beta = beta;
+  P.c = static_cast<float>((a - 1.0) / std::sqrt(static_cast<double>(d)));
+  const cudaError_t e = ea::launch_decode(P, dtype, d, stream);
+  return e == cudaSuccess ? ENTMAX_ATTN_OK : cuda_fail(e);
+}
+
 int entmax_attn_fwd(const void* q, const void* k, const void* v, void* out, float* tau,
                     uint32_t* block_mask, int B, int Hq, int Hkv, int T, int d, float alpha,
                     int n_iter, int causal, const int32_t* cu_seqlens, int dtype,
@@ -637,6 +825,7 @@ const char* entmax_attn_strerror(int code) {
     case ENTMAX_ATTN_ECUDA: return "CUDA runtime error";
     case ENTMAX_ATTN_ETIMEOUT: return "device-side bounded wait timed out";
     case ENTMAX_ATTN_ENOMEM: return "workspace too small or allocation failed";
+    case ENTMAX_ATTN_ERANGE: return "a length, page or slot on the device is out of range";
     default: return "unknown error code";
   }
 }

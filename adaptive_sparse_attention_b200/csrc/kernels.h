@@ -55,6 +55,69 @@ cudaError_t launch_entmax_rows(const void* x, int64_t ldx, void* p, int64_t ldp,
                                int rows, int n, float alpha, int n_iter, int dtype,
                                cudaStream_t s);
 
+// Paged key-value cache (paged.cu, decode.cu).
+constexpr int kMaxRequests = 8192;  // prefix sums over the batch live in shared memory
+
+// Block tables and slot maps of a step (entmax_attn_page_tables).
+struct PageTables {
+  const int32_t* lens;        // [B] tokens held
+  const int32_t* new_lens;    // [B] tokens to add
+  const int32_t* free_pages;  // [n_free]
+  const int32_t* free_start;  // [1] first free entry not yet taken
+  int32_t* tables;            // [B][table_stride]
+  int64_t table_stride;
+  int64_t table_tokens;       // tokens a table row addresses (W page_size)
+  int64_t* slots;             // [n_new], padded: [B][n_new]
+  int32_t* lens_out;          // [B]
+  int32_t* cu_new;            // [B + 1]
+  int32_t* free_next;         // [1]
+  int n_free, B, page_size, n_new, padded;
+};
+cudaError_t launch_page_tables(const PageTables& P, cudaStream_t s);
+
+// New tokens' keys and values into their slots (entmax_attn_paged_append); strides in bytes.
+struct PagedAppend {
+  const void* k;
+  const void* v;
+  void* k_cache;
+  void* v_cache;
+  const int64_t* slots;
+  int* status;
+  int64_t stride_b, stride_h, stride_t;
+  int64_t page_stride, head_stride, slot_stride;
+  int64_t n_slots;  // num_pages page_size
+  int n_tokens, T, Hkv, page_size;
+};
+cudaError_t launch_paged_append(const PagedAppend& P, int row_bytes, cudaStream_t s);
+
+// One-token attention over the paged cache (entmax_attn_decode); strides in elements.
+constexpr int kDecodeScoreWarps = 148 * 16;  // warps of the score kernel: 16 on each SM
+struct DecodeProblem {
+  const void* q;
+  const void* k;
+  const void* v;
+  const int32_t* tables;
+  const int32_t* lens;
+  void* out;
+  float* tau;
+  int* status;
+  int64_t q_stride_b, q_stride_h;
+  int64_t page_stride, head_stride, slot_stride;
+  int64_t table_stride;
+  int num_pages, page_size;
+  int B, Hq, Hkv, G, max_len;
+  int head_blocks, heads_per_block;  // query heads of a kv head are scored 8 or 16 at a time
+  int n_iter;
+  float alpha, beta, c;
+  int score_warps;
+  // workspace
+  int32_t* pre;         // [B + 1] prefix sums of the requests' 16-key units
+  int2* parts;          // [score_warps + B Hkv head_blocks][heads_per_block] (count, max bits)
+  int2* cand;           // [B][Hq][cand_stride] (z bits, key)
+  int64_t cand_stride;  // max_len rounded up to 16
+};
+cudaError_t launch_decode(const DecodeProblem& P, int dtype, int d, cudaStream_t s);
+
 // Records e as the string entmax_attn_last_cuda_error reports and returns ENTMAX_ATTN_ECUDA.
 int record_cuda_error(cudaError_t e);
 

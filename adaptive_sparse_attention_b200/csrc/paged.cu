@@ -1,0 +1,228 @@
+// paged.cu -- the bookkeeping and the writes of a paged key-value cache: block tables and slot
+// maps from the requests' lengths (page_tables_kernel), and the new tokens' keys and values into
+// their slots (paged_append_kernel).
+#include "entmax_attn.h"
+#include "kernels.h"
+
+namespace ea {
+namespace {
+
+constexpr int kTableThreads = 512;
+constexpr int kTableWarps = kTableThreads / 32;
+constexpr unsigned kFull = 0xffffffffu;
+
+struct Grow {
+  int have, need, add;  // pages held, pages needed, new tokens
+  bool ok;              // the lengths make sense and the table row holds the pages
+};
+
+__device__ __forceinline__ Grow grow_of(const PageTables& P, int b) {
+  Grow r;
+  const int len = P.lens[b], add = P.new_lens[b];
+  r.add = max(add, 0);
+  const int64_t total = static_cast<int64_t>(len) + r.add;
+  r.have = len > 0 ? (len - 1) / P.page_size + 1 : 0;
+  r.need = r.have;
+  r.ok = len >= 0 && add >= 0 && total <= P.table_tokens &&
+         (!P.padded || add <= P.n_new);
+  if (r.ok) r.need = total > 0 ? static_cast<int>((total - 1) / P.page_size) + 1 : 0;
+  return r;
+}
+
+// Block-wide inclusive scans of two values at once; totals in tx, ty.
+__device__ __forceinline__ void scan2(int& x, int& y, int2* buf, int& tx, int& ty) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int a = __shfl_up_sync(kFull, x, o), b = __shfl_up_sync(kFull, y, o);
+    if (lane >= o) {
+      x += a;
+      y += b;
+    }
+  }
+  if (lane == 31) buf[warp] = make_int2(x, y);
+  __syncthreads();
+  int bx = 0, by = 0;
+  tx = ty = 0;
+#pragma unroll
+  for (int w = 0; w < kTableWarps; ++w) {
+    const int2 v = buf[w];
+    if (w < warp) {
+      bx += v.x;
+      by += v.y;
+    }
+    tx += v.x;
+    ty += v.y;
+  }
+  x += bx;
+  y += by;
+}
+
+// last b with a[b] <= v (a nondecreasing, a[0] <= v)
+__device__ __forceinline__ int last_at_most(const int* a, int n, int v) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (a[mid] <= v) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+// Every block scans the B lengths itself (a few KB from L2, no second launch and no order between
+// blocks), then writes its share of the new table entries and of the slots.  Bound by the launch
+// and the two dependent loads for small batches, by the slots' writes (8 bytes a token) for large
+// ones.
+__global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTables P) {
+  extern __shared__ int smem[];
+  int* cu = smem;             // [B + 1] first new token of each request
+  int* page0 = smem + P.B + 1;  // [B + 1] first free-list entry of each request, from free_start
+  __shared__ int2 buf[kTableWarps];
+  __shared__ int served_pages;
+  const int tid = threadIdx.x;
+  const int start = *P.free_start;
+  const int avail = start >= 0 && start <= P.n_free ? P.n_free - start : 0;
+  if (tid == 0) served_pages = 0;
+  {
+    const int per = (P.B + kTableThreads - 1) / kTableThreads;
+    const int b0 = min(tid * per, P.B), b1 = min(b0 + per, P.B);
+    int toks = 0, pages = 0;
+    for (int b = b0; b < b1; ++b) {
+      const Grow r = grow_of(P, b);
+      toks += r.add;
+      pages += r.need - r.have;
+    }
+    int x = toks, y = pages, tx, ty;
+    scan2(x, y, buf, tx, ty);
+    x -= toks;
+    y -= pages;
+    for (int b = b0; b < b1; ++b) {
+      const Grow r = grow_of(P, b);
+      cu[b] = x;
+      page0[b] = y;
+      x += r.add;
+      y += r.need - r.have;
+    }
+    if (tid == 0) {
+      cu[P.B] = tx;
+      page0[P.B] = ty;
+    }
+    __syncthreads();
+  }
+  // A request is served if its lengths fit, its tokens lie inside the slots and its pages inside
+  // the free list.  Requests that take pages are served in order until the list is exhausted.
+  auto served = [&](int b, const Grow& r) {
+    return r.ok && (P.padded || cu[b + 1] <= P.n_new) &&
+           (r.need == r.have || page0[b + 1] <= avail);
+  };
+  if (blockIdx.x == 0) {
+    int most = 0;
+    for (int b = tid; b < P.B; b += kTableThreads) {
+      const Grow r = grow_of(P, b);
+      const bool s = served(b, r);
+      P.lens_out[b] = P.lens[b] + (s ? r.add : 0);
+      P.cu_new[b] = cu[b];
+      if (s && r.need > r.have) most = max(most, page0[b + 1]);
+    }
+    atomicMax(&served_pages, most);  // the order does not matter to a maximum
+    __syncthreads();
+    if (tid == 0) {
+      P.cu_new[P.B] = cu[P.B];
+      *P.free_next = start + served_pages;
+    }
+  }
+  const int64_t step = static_cast<int64_t>(gridDim.x) * kTableThreads;
+  const int64_t me = static_cast<int64_t>(blockIdx.x) * kTableThreads + tid;
+  // new table entries
+  const int n_pages = min(page0[P.B], avail);
+  for (int64_t j = me; j < n_pages; j += step) {
+    const int b = last_at_most(page0, P.B, static_cast<int>(j));
+    const Grow r = grow_of(P, b);
+    if (served(b, r))
+      P.tables[b * P.table_stride + r.have + (static_cast<int>(j) - page0[b])] =
+          P.free_pages[start + j];
+  }
+  // slots
+  const int64_t n_slots = P.padded ? static_cast<int64_t>(P.B) * P.n_new : P.n_new;
+  for (int64_t i = me; i < n_slots; i += step) {
+    int b, t;
+    if (P.padded) {
+      b = static_cast<int>(i / P.n_new);
+      t = static_cast<int>(i - static_cast<int64_t>(b) * P.n_new);
+    } else {
+      b = last_at_most(cu, P.B, static_cast<int>(i));
+      t = static_cast<int>(i) - cu[b];
+    }
+    const Grow r = grow_of(P, b);
+    int64_t slot = -1;
+    if (t < r.add && served(b, r)) {
+      const int pos = P.lens[b] + t;
+      const int blk = pos / P.page_size;
+      const int page = blk < r.have ? P.tables[b * P.table_stride + blk]
+                                    : P.free_pages[start + page0[b] + (blk - r.have)];
+      if (page >= 0)
+        slot = static_cast<int64_t>(page) * P.page_size + (pos - blk * P.page_size);
+    }
+    P.slots[i] = slot;
+  }
+}
+
+// One 16-byte vector of one (token, kv head) row of k or v per thread and step; a row's vectors
+// are consecutive lanes.  A pure copy: bound by HBM.
+template <int VPR>  // 16-byte vectors per row
+__global__ void __launch_bounds__(256) paged_append_kernel(const PagedAppend P) {
+  const int64_t rows = static_cast<int64_t>(P.n_tokens) * P.Hkv;
+  const int64_t per_grid = static_cast<int64_t>(gridDim.x) * (256 / VPR);
+  const int lane = threadIdx.x % VPR;
+  const char* src = static_cast<const char*>(blockIdx.y ? P.v : P.k) + lane * 16;
+  char* dst = static_cast<char*>(blockIdx.y ? P.v_cache : P.k_cache) + lane * 16;
+  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / VPR) + threadIdx.x / VPR; r < rows;
+       r += per_grid) {
+    const int h = static_cast<int>(r / P.n_tokens);
+    const int n = static_cast<int>(r - static_cast<int64_t>(h) * P.n_tokens);
+    const int64_t slot = P.slots[n];
+    if (slot < 0) continue;  // a padding row
+    if (slot >= P.n_slots) {
+      if (lane == 0) atomicMax(P.status, ENTMAX_ATTN_ERANGE);
+      continue;
+    }
+    const int b = n / P.T, t = n - b * P.T;
+    const int64_t page = slot / P.page_size;
+    const int off = static_cast<int>(slot - page * P.page_size);
+    const uint4 x = *reinterpret_cast<const uint4*>(src + b * P.stride_b + h * P.stride_h +
+                                                    t * P.stride_t);
+    *reinterpret_cast<uint4*>(dst + page * P.page_stride + h * P.head_stride +
+                              off * P.slot_stride) = x;
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_page_tables(const PageTables& P, cudaStream_t s) {
+  const int64_t n_slots = P.padded ? static_cast<int64_t>(P.B) * P.n_new : P.n_new;
+  const int64_t want = (n_slots + kTableThreads - 1) / kTableThreads;
+  const int grid = static_cast<int>(want < 1 ? 1 : want > 148 ? 148 : want);
+  const size_t smem = 2 * sizeof(int) * (P.B + 1);
+  if (smem > 48 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
+  page_tables_kernel<<<grid, kTableThreads, smem, s>>>(P);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_paged_append(const PagedAppend& P, int row_bytes, cudaStream_t s) {
+  const int vpr = row_bytes / 16;
+  const int64_t rows = static_cast<int64_t>(P.n_tokens) * P.Hkv;
+  const int64_t want = (rows * vpr + 255) / 256;
+  const dim3 grid(static_cast<unsigned>(want > 148 * 8 ? 148 * 8 : want), 2);
+  switch (vpr) {
+    case 8: paged_append_kernel<8><<<grid, 256, 0, s>>>(P); break;
+    case 16: paged_append_kernel<16><<<grid, 256, 0, s>>>(P); break;
+    default: paged_append_kernel<32><<<grid, 256, 0, s>>>(P);
+  }
+  return cudaGetLastError();
+}
+
+}  // namespace ea

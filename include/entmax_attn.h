@@ -67,6 +67,8 @@ extern "C" {
 #define ENTMAX_ATTN_ECUDA 3    /* a CUDA runtime call failed (see entmax_attn_last_cuda_error) */
 #define ENTMAX_ATTN_ETIMEOUT 4 /* a device-side bounded wait gave up (status word) */
 #define ENTMAX_ATTN_ENOMEM 5   /* workspace too small, or the library's allocation failed */
+#define ENTMAX_ATTN_ERANGE 6   /* a length, page or slot read on the device was out of range
+                                  (status word; the paged-cache entry points) */
 
 /* dtype codes. */
 #define ENTMAX_ATTN_FP32 0
@@ -256,8 +258,98 @@ int entmax_attn_route_chunks(const void* q, const void* summaries, float* pi, fl
                              int n_iter, int causal, int estimate_diagonal, float scaling_factor,
                              int dtype, cudaStream_t stream);
 
+/* ------------------------------------------------------------------ paged key-value cache --
+ *
+ * Serving: the keys and values of many requests of different lengths live in pages of page_size
+ * tokens.  k_cache and v_cache hold num_pages pages; element e of (page, kv head, slot) is at
+ * page * page_stride + head * head_stride + slot * slot_stride + e (strides in elements, the same
+ * for both, multiples of 16 bytes and at least d; so both [pages, Hkv, page_size, d] and
+ * [pages, page_size, Hkv, d] caches work).  block_tables int32 [B][table_stride], W <= table_stride
+ * of each row in use, lists a request's pages in order: key j is in slot j % page_size of page
+ * block_tables[b][j / page_size].  A token's "slot" is page * page_size + (slot in the page).
+ * Any page_size >= 1; B at most 8192.
+ *
+ * A step of a server: entmax_attn_page_tables from the lengths, entmax_attn_paged_append of the
+ * new tokens' k and v, then entmax_attn_fwd over the packed prompts (its cu_seqlens is cu_new)
+ * and entmax_attn_decode for the requests that grew by one token.
+ */
+
+/* Block tables and slot maps of a step, built on the device from the requests' lengths.
+ * Request b holds lens[b] tokens and gets new_lens[b] more.  With P = page_size,
+ * have = ceil(lens[b] / P) and need = ceil((lens[b] + new_lens[b]) / P), it takes need - have pages
+ * from the free list: the requests' takes are laid out one after the other from entry
+ * *free_start of free_pages, and written to columns [have, need) of its table row; no other entry
+ * is written.
+ *   slots:  padded = 0: int64 [n_new], the new tokens of all requests packed in order (request b's
+ *           start at cu_new[b]), -1 behind the last; padded = 1: int64 [B][n_new], token t of
+ *           request b at [b][t], -1 for t >= new_lens[b].
+ *   lens_out int32 [B]: the lengths after the step.  cu_new int32 [B + 1]: prefix sums of new_lens.
+ *   free_next int32 [1]: free_start after the step.
+ * A request that does not fit keeps its length, takes no page, and its tokens get slot -1: one
+ * whose lengths are negative or exceed W * page_size tokens, whose tokens lie beyond the slots, or
+ * whose pages lie beyond entry n_free (requests are served in order; once one runs out of pages,
+ * so does every later one that needs a page).  A token whose page is a table entry below 0 gets
+ * slot -1.  The sums of new_lens and B * W must stay below 2^31.
+ * Outputs may not overlap inputs (block_tables is both).  Device pointers, aligned to their
+ * element size; asynchronous on `stream`.  Returns ENTMAX_ATTN_OK, ENTMAX_ATTN_EINVAL (null pointer,
+ * size < 1, n_free < 0, B > 8192, table_stride < W, padded not 0/1, lens_out == lens or new_lens,
+ * free_next == free_start), ENTMAX_ATTN_EALIGN or ENTMAX_ATTN_ECUDA. */
+int entmax_attn_page_tables(const int32_t* lens, const int32_t* new_lens,
+                            const int32_t* free_pages, int n_free, const int32_t* free_start,
+                            int32_t* block_tables, long long table_stride, int W, int B,
+                            int page_size, int64_t* slots, int n_new, int padded,
+                            int32_t* lens_out, int32_t* cu_new, int32_t* free_next,
+                            cudaStream_t stream);
+
+/* Stores the new tokens' keys and values in their slots.  k and v: element e of (batch row b, kv
+ * head h, token t) at b * stride_b + h * stride_h + t * stride_t + e (strides in elements, the same
+ * for both, multiples of 16 bytes), B batch rows of T tokens: [B, Hkv, T, d], or packed
+ * [Hkv, T, d] with B = 1.  slots int64 [B * T], token (b, t) at b * T + t; a negative slot skips
+ * the token, one at or beyond num_pages * page_size skips it and latches ENTMAX_ATTN_ERANGE in the
+ * status word.  The slots of one call must differ (of a slot given twice, either token's row or a
+ * mixture of both is stored).  dtype ENTMAX_ATTN_FP32 or ENTMAX_ATTN_BF16 throughout; d 64 or 128.
+ * Device pointers, 16-byte aligned (slots 8); asynchronous on `stream`.  Returns ENTMAX_ATTN_OK,
+ * ENTMAX_ATTN_EINVAL (null pointer, size < 1, B * T >= 2^31, bad d, dtype or stride) ,
+ * ENTMAX_ATTN_EALIGN or ENTMAX_ATTN_ECUDA. */
+int entmax_attn_paged_append(const void* k, const void* v, long long stride_b, long long stride_h,
+                             long long stride_t, void* k_cache, void* v_cache,
+                             long long page_stride, long long head_stride, long long slot_stride,
+                             int num_pages, int page_size, const int64_t* slots, int B, int Hkv,
+                             int T, int d, int dtype, cudaStream_t stream);
+
+/* Bytes of workspace entmax_attn_decode needs for requests of up to max_len tokens; 0 on bad
+ * sizes. */
+size_t entmax_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int max_len);
+
+/* alpha-entmax attention of one new token per request over its paged keys and values: the forward
+ * pass for q of one row per (request, head), which sees all seq_lens[b] keys.
+ *   q: element e of (b, h) at b * q_stride_b + h * q_stride_h + e (strides in elements, multiples of
+ *      16 bytes); out [B, Hq, d] contiguous, q's dtype; tau fp32 [B, Hq].
+ *   seq_lens int32 [B], at most max_len <= W * page_size.
+ * A request of length 0 (an unused row of the batch) has out = 0 and tau = +inf.  Only the values
+ * of keys with p > 0 are read.  A score that is NaN or +inf makes out and tau of its (request,
+ * head) NaN.  A length outside [0, max_len] or a page outside [0, num_pages) makes those of the
+ * request NaN and latches ENTMAX_ATTN_ERANGE in the status word; nothing outside the cache is read.
+ * workspace: device memory of entmax_attn_decode_workspace_bytes(...), 256-byte aligned, owned by
+ * the caller, needed until the call's work has completed; its contents need not be initialised or
+ * kept.  Calls that overlap on the device need workspaces of their own.  The same inputs give the
+ * same bits.
+ * Device pointers, 16-byte aligned (block_tables, seq_lens, tau 4); asynchronous on `stream`, no host
+ * synchronisation, so it can be captured into a graph and replayed as the lengths grow up to
+ * max_len.  Returns ENTMAX_ATTN_OK, ENTMAX_ATTN_EINVAL (null pointer, size < 1, B > 8192,
+ * Hq % Hkv != 0, d not 64 or 128, bad stride, max_len > W * page_size, alpha <= 1 or not finite,
+ * n_iter outside [1, 1000], bad dtype), ENTMAX_ATTN_EALIGN, ENTMAX_ATTN_ENOMEM (workspace too
+ * small) or ENTMAX_ATTN_ECUDA. */
+int entmax_attn_decode(const void* q, long long q_stride_b, long long q_stride_h,
+                       const void* k_cache, const void* v_cache, long long page_stride,
+                       long long head_stride, long long slot_stride, int num_pages, int page_size,
+                       const int32_t* block_tables, long long table_stride, int W,
+                       const int32_t* seq_lens, void* out, float* tau, void* workspace,
+                       size_t workspace_bytes, int B, int Hq, int Hkv, int max_len, int d,
+                       float alpha, int n_iter, int dtype, cudaStream_t stream);
+
 /* Synchronises `stream`, returns the device status word of the current device
- * (ENTMAX_ATTN_OK or ENTMAX_ATTN_ETIMEOUT) and clears it. */
+ * (ENTMAX_ATTN_OK, ENTMAX_ATTN_ETIMEOUT or ENTMAX_ATTN_ERANGE) and clears it. */
 int entmax_attn_status(cudaStream_t stream);
 
 /* Frees the workspaces entmax_attn_fwd cached (synchronises the device first). */

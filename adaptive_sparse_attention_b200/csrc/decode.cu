@@ -28,9 +28,10 @@ namespace {
 
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kJoinThreads = 128;
+constexpr int kJoinThreads = 256;
 constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kWarpList = 512;  // candidates a warp of the join keeps in shared memory
+constexpr int kWarpList = 256;  // candidates a warp of the join keeps in shared memory
+constexpr int kNewtonSteps = 64;  // a bound that no search reaches
 constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ int clamped_len(const DecodeProblem& P, int b) {
@@ -93,8 +94,12 @@ template <int D, int NT>
 struct Scorer<__nv_bfloat16, D, NT> {
   static constexpr int kChunks = D / 32;  // 16-byte chunks per lane and row
   uint32_t bq[NT][kChunks][4];
-  __device__ __forceinline__ void load_q(const __nv_bfloat16* q, int64_t stride_h, int heads,
-                                         float*) {
+  // q of head group hg of request b
+  __device__ __forceinline__ void load_q(const DecodeProblem& P, int b, int hg, float*) {
+    const int hk = hg / P.head_blocks, first = (hg - hk * P.head_blocks) * 8 * NT;
+    const int heads = P.G - first;
+    const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(P.q) + b * P.q_stride_b +
+                             (hk * P.G + first) * P.q_stride_h;
     const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -102,7 +107,7 @@ struct Scorer<__nv_bfloat16, D, NT> {
       for (int c = 0; c < kChunks; ++c) {
         uint4 x = make_uint4(0u, 0u, 0u, 0u);
         if (n * 8 + g < heads)
-          x = *reinterpret_cast<const uint4*>(q + (n * 8 + g) * stride_h + c * 32 + t * 8);
+          x = *reinterpret_cast<const uint4*>(q + (n * 8 + g) * P.q_stride_h + c * 32 + t * 8);
         bq[n][c][0] = x.x;
         bq[n][c][1] = x.y;
         bq[n][c][2] = x.z;
@@ -127,13 +132,16 @@ template <int D, int NT>
 struct Scorer<float, D, NT> {
   static constexpr int kChunks = D / 16;
   int heads_;
-  // q of the group's heads into the warp's shared-memory rows [8 NT][D]
-  __device__ __forceinline__ void load_q(const float* q, int64_t stride_h, int heads, float* sq) {
+  // q of head group hg of request b into the warp's shared-memory rows [8 NT][D]
+  __device__ __forceinline__ void load_q(const DecodeProblem& P, int b, int hg, float* sq) {
+    const int hk = hg / P.head_blocks, first = (hg - hk * P.head_blocks) * 8 * NT;
+    heads_ = min(8 * NT, P.G - first);
+    const float* q = static_cast<const float*>(P.q) + b * P.q_stride_b +
+                     (hk * P.G + first) * P.q_stride_h;
     __syncwarp();
-    heads_ = heads;
-    for (int i = threadIdx.x & 31; i < heads * (D / 4); i += 32)
+    for (int i = threadIdx.x & 31; i < heads_ * (D / 4); i += 32)
       reinterpret_cast<float4*>(sq)[i] = *reinterpret_cast<const float4*>(
-          q + (i / (D / 4)) * stride_h + (i % (D / 4)) * 4);
+          q + (i / (D / 4)) * P.q_stride_h + (i % (D / 4)) * 4);
     __syncwarp();
   }
   __device__ __forceinline__ void scores(const uint4 (&a)[2][kChunks], float (&acc)[NT][4],
@@ -172,12 +180,6 @@ struct Scorer<float, D, NT> {
   }
 };
 
-// The two key rows a lane reads of one unit, and whether they exist.
-template <int CH>
-struct Unit {
-  uint4 a[2][CH];
-};
-
 // Walks the block table for one key row of a lane: the row of unit u + 1 is 16 keys further on.
 struct RowCursor {
   int blk, off;
@@ -200,12 +202,418 @@ struct RowCursor {
   }
 };
 
+// One warp scores units [first, last) of 16 keys of head group hg of request b and appends the
+// candidates of each head to the group's lists at the run's first key, a count and a max per head
+// to part.  sq: the warp's (or block's) shared-memory q rows, fp32 only.
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(kScoreThreads, 4) decode_scores_kernel(const DecodeProblem P) {
+__device__ __forceinline__ void score_run(const DecodeProblem& P,
+                                          const Scorer<T, D, NT>& sc, const float* sq, int b,
+                                          int hg, int len, int first, int last, int2* part) {
   using S = Scorer<T, D, NT>;
   constexpr int CH = S::kChunks;
   // 8 KB of keys in flight per warp
   constexpr int DEPTH = 8192 / (16 * D * static_cast<int>(sizeof(T)));
+  const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  const int hk = hg / P.head_blocks, hb = hg - hk * P.head_blocks;
+  const int h0 = hk * P.G + hb * 8 * NT;
+  const int heads = min(8 * NT, P.G - hb * 8 * NT);
+  const int32_t* table = P.tables + b * P.table_stride;
+  const T* kbase = static_cast<const T*>(P.k) + hk * P.head_stride + t * (16 / sizeof(T));
+
+  float m[NT][2];
+  int cnt[NT][2];
+  bool bad[NT][2];
+  int2* cand[NT][2];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      m[n][e] = -INFINITY;
+      cnt[n][e] = 0;
+      bad[n][e] = false;
+      const int h = n * 8 + 2 * t + e;
+      cand[n][e] = P.cand + (static_cast<int64_t>(b) * P.Hq + h0 + min(h, heads - 1)) *
+                                P.cand_stride + first * 16;
+    }
+  bool bad_page = false;
+
+  // Pipeline: the keys of the next DEPTH units are in registers or on their way, the page numbers
+  // of the unit after those too.
+  RowCursor cur[2];
+  cur[0].start(first * 16 + g, P.page_size);
+  cur[1].start(first * 16 + g + 8, P.page_size);
+  int fetch = first;  // unit the cursors stand at
+  int page[2], off[2];
+  auto next_pages = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      page[i] = -1;
+      off[i] = cur[i].off;
+      if (fetch < last && fetch * 16 + g + 8 * i < len) {
+        page[i] = table[cur[i].blk];
+        if (page[i] < 0 || page[i] >= P.num_pages) {
+          page[i] = -1;
+          bad_page = true;
+        }
+      }
+      cur[i].advance(P.page_size);
+    }
+    ++fetch;
+  };
+  uint4 unit[DEPTH][2][CH];
+  auto load_unit = [&](uint4 (&x)[2][CH]) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const T* row = kbase + page[i] * P.page_stride + off[i] * P.slot_stride;
+#pragma unroll
+      for (int c = 0; c < CH; ++c)
+        x[i][c] = page[i] >= 0 ? load_stream(row + c * (64 / sizeof(T)))
+                               : make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  next_pages();
+#pragma unroll
+  for (int i = 0; i < DEPTH; ++i) {
+    load_unit(unit[i]);
+    next_pages();
+  }
+  for (int blk0 = first; blk0 < last; blk0 += DEPTH) {
+#pragma unroll
+    for (int i = 0; i < DEPTH; ++i) {
+      const int blk = blk0 + i;
+      if (blk < last) {
+        float acc[NT][4];
+        sc.scores(unit[i], acc, sq);
+        load_unit(unit[i]);
+        next_pages();
+        const int key = blk * 16 + g;
+        bool pass = false;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const bool live = n * 8 + 2 * t + (e & 1) < heads && key + (e >> 1) * 8 < len;
+            const float z = live ? P.c * acc[n][e] : -INFINITY;
+            acc[n][e] = z;
+            bad[n][e & 1] |= !(z < INFINITY);
+            pass |= z > m[n][e & 1] - 1.f;
+          }
+        if (__any_sync(kFull, pass)) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float x = fmaxf(acc[n][e], acc[n][2 + e]);
+#pragma unroll
+              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+              m[n][e] = fmaxf(m[n][e], x);
+#pragma unroll
+              for (int r = 0; r < 2; ++r) {
+                const float z = acc[n][2 * r + e];
+                const bool in = z > m[n][e] - 1.f;
+                const unsigned mine = __ballot_sync(kFull, in) & (0x11111111u << t);
+                if (in)
+                  cand[n][e][cnt[n][e] + __popc(mine & ((1u << lane) - 1u))] =
+                      make_int2(__float_as_int(z), key + 8 * r);
+                cnt[n][e] += __popc(mine);
+              }
+            }
+        }
+      }
+    }
+  }
+  bad_page = __any_sync(kFull, bad_page);
+  if (bad_page && lane == 0) atomicMax(P.status, ENTMAX_ATTN_ERANGE);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const bool nan = (__ballot_sync(kFull, bad[n][e]) & (0x11111111u << t)) != 0u || bad_page;
+      if (g == 0)
+        part[n * 8 + 2 * t + e] = make_int2(cnt[n][e], __float_as_int(nan ? NAN : m[n][e]));
+    }
+}
+
+// max that keeps a NaN of either side
+__device__ __forceinline__ float max_nan(float a, float b) {
+  return (a != a || b != b) ? NAN : fmaxf(a, b);
+}
+
+// x^beta for x > 0 (or 0 where x <= 0), to a few units of the last place: near beta = 3 the cube
+// times x^(beta - 3), whose exponent is small enough for the fast logarithm's error.
+template <int BK>
+__device__ __forceinline__ float power(float x, float beta) {
+  if (!(x > 0.f)) return 0.f;
+  if (BK == kBetaOne) return x;
+  if (BK == kBetaTwo) return x * x;
+  if (BK == kBetaNear3) return (x * x) * (x * exp2f((beta - 3.f) * __log2f(x)));
+  return exp2f(beta * log2f(x));
+}
+
+struct JoinSmem {
+  float2 list[kJoinWarps][kWarpList];  // (z, key bits): each warp's candidates
+  float2 sums[2][kJoinWarps];
+  float sums2[2][kJoinWarps];
+  float red[kJoinWarps];
+  float2 live[kJoinWarps][32];  // (p, -) and offsets of the values being added
+  int64_t from[kJoinWarps][32];
+  __align__(16) float o[kJoinWarps][128];
+};
+
+// One block joins the parts of one (request, query head): part(i) is its i-th count and max,
+// key0(i) the first key of part i in the candidate list.
+template <typename T, int D, int BK, typename Part, typename Key0>
+__device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem& sm, int b, int h,
+                                          int len, int np, const Part& part, const Key0& key0) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int hk = h / P.G;
+  const int64_t row = static_cast<int64_t>(b) * P.Hq + h;
+  T* out = static_cast<T*>(P.out) + row * D;
+
+  float m = -INFINITY;
+  for (int i = tid; i < np; i += kJoinThreads) m = max_nan(m, __int_as_float(part(i).y));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
+  if (lane == 0) sm.red[warp] = m;
+  __syncthreads();
+  m = sm.red[0];
+#pragma unroll
+  for (int i = 1; i < kJoinWarps; ++i) m = max_nan(m, sm.red[i]);
+  if (!(m > -INFINITY)) {  // NaN, or every score -inf: p is not defined
+    for (int i = tid; i < D; i += kJoinThreads) store_elem(out, i, NAN);
+    if (tid == 0) P.tau[row] = NAN;
+    return;
+  }
+
+  // Each warp compacts the entries with z > m - 1 of a contiguous range of parts, in order: the
+  // first kWarpList into shared memory, the others back to the front of the range (an entry only
+  // moves forward, over entries that the warp has read already).
+  int2* cand = P.cand + row * P.cand_stride;
+  const int i_end = static_cast<int>(static_cast<int64_t>(warp + 1) * np / kJoinWarps);
+  const int i_beg = static_cast<int>(static_cast<int64_t>(warp) * np / kJoinWarps);
+  int2* spill = cand + (i_beg < i_end ? key0(i_beg) : 0);
+  int n_list = 0;
+  for (int i0 = i_beg; i0 < i_end; i0 += 32) {
+    int n = 0;
+    int64_t k0 = 0;
+    if (i0 + lane < i_end) {
+      const int2 x = part(i0 + lane);
+      if (__int_as_float(x.y) > m - 1.f) n = x.x;
+      k0 = key0(i0 + lane);
+    }
+    int start = n;  // of this lane's part in the sequence of the 32 parts' entries
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, start, o);
+      if (lane >= o) start += y;
+    }
+    const int total = __shfl_sync(kFull, start, 31);
+    start -= n;
+    const int64_t shift = k0 - start;
+    constexpr int U = 4;  // loads in flight per lane
+    for (int e0 = 0; e0 < total; e0 += 32 * U) {
+      int2 x[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int e = e0 + 32 * j + lane;
+        int lo = 0;  // the last part that starts at or before e
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1)
+          if (__shfl_sync(kFull, start, lo + o) <= e) lo += o;
+        const int64_t at = __shfl_sync(kFull, shift, lo) + e;
+        x[j] = make_int2(__float_as_int(-INFINITY), 0);
+        if (e < total) x[j] = cand[at];
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const bool in = __int_as_float(x[j].x) > m - 1.f;
+        const unsigned bal = __ballot_sync(kFull, in);
+        const int at = n_list + __popc(bal & ((1u << lane) - 1u));
+        if (in) {
+          if (at < kWarpList)
+            sm.list[warp][at] = make_float2(__int_as_float(x[j].x), __int_as_float(x[j].y));
+          else
+            spill[at - kWarpList] = x[j];
+        }
+        n_list += __popc(bal);
+      }
+    }
+  }
+  __syncwarp();
+  auto entry = [&](int e) {
+    if (e < kWarpList) return sm.list[warp][e];
+    const int2 x = spill[e - kWarpList];
+    return make_float2(__int_as_float(x.x), __int_as_float(x.y));
+  };
+
+  // tau.  For beta >= 1 by Newton's steps on the norm g(tau) = (sum [z - tau]_+^beta)^(1/beta) = 1
+  // from tau = m - 1, where g >= 1: g is convex and falling (a norm of functions that are), so
+  // the iterates rise to the root and never pass it, and it is linear in tau while the support
+  // stays and the scores tie, so the steps are few: with S0, S1 the sums of the powers beta and
+  // beta - 1, (g - 1) / -g' = (S0 - S0^(1 - 1/beta)) / S1.  They run until tau has settled (4 or 5
+  // steps on normal scores, 14 at most over a wide sweep of sizes and spreads at beta = 1), so
+  // n_iter does not enter.  For beta < 1 g is not convex, and the bracketed search of the
+  // attention passes is used.
+  float tau;
+  if (BK != kBetaGeneral || P.beta >= 1.f) {
+    tau = m - 1.f;
+    for (int it = 0; it < kNewtonSteps; ++it) {
+      float s0 = 0.f, s1 = 0.f;
+      for (int e = lane; e < n_list; e += 32) {
+        const float y = entry(e).x - tau;
+        if (BK == kBetaOne) {
+          if (y > 0.f) {
+            s0 += y;
+            s1 += 1.f;
+          }
+        } else if (BK == kBetaTwo) {
+          const float x = fmaxf(y, 0.f);
+          s1 += x;
+          s0 = fmaf(x, x, s0);
+        } else if (y > 0.f) {
+          const float p = power<BK>(y, P.beta);
+          s0 += p;
+          s1 += __fdividef(p, y);
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        s0 += __shfl_xor_sync(kFull, s0, o);
+        s1 += __shfl_xor_sync(kFull, s1, o);
+      }
+      if (lane == 0) sm.sums[it & 1][warp] = make_float2(s0, s1);
+      __syncthreads();  // two buffers: the next step writes the other one
+      s0 = s1 = 0.f;
+#pragma unroll
+      for (int i = 0; i < kJoinWarps; ++i) {
+        s0 += sm.sums[it & 1][i].x;
+        s1 += sm.sums[it & 1][i].y;
+      }
+      float step;
+      if (BK == kBetaOne) step = (s0 - 1.f) / s1;
+      else if (BK == kBetaTwo) step = (s0 - sqrtf(s0)) / s1;
+      else step = (s0 - exp2f((1.f - 1.f / P.beta) * log2f(s0))) / s1;
+      tau += step;
+      if (!(step > 2.f * FLT_EPSILON * fmaxf(fabsf(tau), m - tau))) break;
+    }
+  } else {
+    Search sr;
+    sr.init(m, len, P.alpha);
+    for (int it = 0; it < P.n_iter; ++it) {
+      float s0 = 0.f, s1 = 0.f, s2 = 0.f;
+      for (int e = lane; e < n_list; e += 32) {
+        const float y = entry(e).x - sr.tau;
+        if (y > 0.f) {
+          float p0, p1, p2;
+          entmax_powers<BK>(y, P.beta, p0, p1, p2);
+          s0 += p0;
+          s1 += p1;
+          s2 += p2;
+        }
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) {
+        s0 += __shfl_xor_sync(kFull, s0, o);
+        s1 += __shfl_xor_sync(kFull, s1, o);
+        s2 += __shfl_xor_sync(kFull, s2, o);
+      }
+      if (lane == 0) {
+        sm.sums[it & 1][warp] = make_float2(s0, s1);
+        sm.sums2[it & 1][warp] = s2;
+      }
+      __syncthreads();
+      s0 = s1 = s2 = 0.f;
+#pragma unroll
+      for (int i = 0; i < kJoinWarps; ++i) {
+        s0 += sm.sums[it & 1][i].x;
+        s1 += sm.sums[it & 1][i].y;
+        s2 += sm.sums2[it & 1][i];
+      }
+      sr.step<BK>(s0, s1, s2, P.beta);
+      if (sr.settled()) break;
+    }
+    tau = sr.tau;
+  }
+
+  // o: each warp adds the values of its entries with p > 0, in 16-byte chunks, D sizeof(T) / 16
+  // lanes per row, four rows per lane group in flight
+  constexpr int LPR = D * sizeof(T) / 16;  // lanes per value row (8, 16 or 32)
+  constexpr int RPW = 32 / LPR;            // value rows per warp load
+  constexpr int EPL = 16 / sizeof(T);      // elements per lane
+  constexpr int U = 4;
+  float o[EPL] = {};
+  const int32_t* table = P.tables + b * P.table_stride;
+  const T* vbase = static_cast<const T*>(P.v) + hk * P.head_stride + (lane % LPR) * EPL;
+  for (int e0 = 0; e0 < n_list; e0 += 32) {
+    float p = 0.f;
+    int key = 0;
+    if (e0 + lane < n_list) {
+      const float2 x = entry(e0 + lane);
+      p = power<BK>(x.x - tau, P.beta);
+      key = __float_as_int(x.y);
+    }
+    const unsigned live = __ballot_sync(kFull, p > 0.f);
+    if (!live) continue;
+    const int n = __popc(live);
+    if (p > 0.f) {
+      const int at = __popc(live & ((1u << lane) - 1u));
+      const int blk = key / P.page_size;
+      sm.live[warp][at].x = p;
+      sm.from[warp][at] = table[blk] * P.page_stride + (key - blk * P.page_size) * P.slot_stride;
+    }
+    __syncwarp();
+    for (int i0 = 0; i0 < n; i0 += RPW * U) {
+      uint4 x[U];
+      float w[U];
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const int i = i0 + j * RPW + lane / LPR;
+        w[j] = 0.f;
+        x[j] = make_uint4(0u, 0u, 0u, 0u);
+        if (i < n) {
+          w[j] = sm.live[warp][i].x;
+          x[j] = load_stream(vbase + sm.from[warp][i]);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j) {
+        const T* v = reinterpret_cast<const T*>(&x[j]);
+#pragma unroll
+        for (int i = 0; i < EPL; ++i) o[i] = fmaf(w[j], load_elem(v, i), o[i]);
+      }
+    }
+    __syncwarp();
+  }
+#pragma unroll
+  for (int s = LPR; s < 32; s <<= 1)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) o[i] += __shfl_xor_sync(kFull, o[i], s);
+  if (lane < LPR)
+#pragma unroll
+    for (int i = 0; i < EPL; ++i) sm.o[warp][lane * EPL + i] = o[i];
+  __syncthreads();
+  for (int i = tid; i < D; i += kJoinThreads) {
+    float s = 0.f;
+#pragma unroll
+    for (int k = 0; k < kJoinWarps; ++k) s += sm.o[k][i];
+    store_elem(out, i, s);
+  }
+  if (tid == 0) P.tau[row] = tau;
+}
+
+// o and tau of a request without keys (o = 0, tau = +inf) or with a length out of range (NaN)
+template <typename T, int D>
+__device__ __forceinline__ void write_empty(const DecodeProblem& P, int b, int h, bool valid) {
+  const int64_t row = static_cast<int64_t>(b) * P.Hq + h;
+  T* out = static_cast<T*>(P.out) + row * D;
+  for (int i = threadIdx.x; i < D; i += kJoinThreads) store_elem(out, i, valid ? 0.f : NAN);
+  if (threadIdx.x == 0) P.tau[row] = valid ? INFINITY : NAN;
+}
+
+// ------------------------------------------------------------------ split: two kernels --
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kScoreThreads, 4) decode_scores_kernel(const DecodeProblem P) {
   extern __shared__ __align__(16) char smem[];
   float* sq_all = reinterpret_cast<float*>(smem);  // fp32 only: [warps][8 NT][D]
   int* pre = reinterpret_cast<int*>(
@@ -213,8 +621,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) decode_scores_kernel(const D
   __shared__ int scan_buf[kScoreWarps];
   asm volatile("griddepcontrol.launch_dependents;");
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, t = lane & 3;
+  const int tid = threadIdx.x, warp = tid >> 5;
   {  // prefix sums of the requests' unit counts
     const int per = (P.B + kScoreThreads - 1) / kScoreThreads;
     const int b0 = min(tid * per, P.B), b1 = min(b0 + per, P.B);
@@ -260,163 +667,26 @@ __global__ void __launch_bounds__(kScoreThreads, 4) decode_scores_kernel(const D
     const int first = static_cast<int>(r - static_cast<int64_t>(hg) * nb);
     const int last = static_cast<int>(min(static_cast<int64_t>(nb), first + (u_end - u)));
     u += last - first;
-    const int hk = hg / P.head_blocks, hb = hg - hk * P.head_blocks;
-    const int h0 = hk * P.G + hb * 8 * NT;               // first query head of the part
-    const int heads = min(8 * NT, P.G - hb * 8 * NT);    // its query heads
-    const int len = clamped_len(P, b);
-    const int32_t* table = P.tables + b * P.table_stride;
-    const T* kbase = static_cast<const T*>(P.k) + hk * P.head_stride + t * (16 / sizeof(T));
-    S sc;
-    sc.load_q(static_cast<const T*>(P.q) + b * P.q_stride_b + h0 * P.q_stride_h, P.q_stride_h,
-              heads, sq);
-
-    float m[NT][2];
-    int cnt[NT][2];
-    bool bad[NT][2];
-    int2* cand[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        m[n][e] = -INFINITY;
-        cnt[n][e] = 0;
-        bad[n][e] = false;
-        const int h = n * 8 + 2 * t + e;
-        cand[n][e] = P.cand + (static_cast<int64_t>(b) * P.Hq + h0 + min(h, heads - 1)) *
-                                  P.cand_stride + first * 16;
-      }
-    bool bad_page = false;
-
-    // Pipeline: the keys of the next DEPTH units are in registers or on their way, the page
-    // numbers of the unit after those too.
-    RowCursor cur[2];
-    cur[0].start(first * 16 + g, P.page_size);
-    cur[1].start(first * 16 + g + 8, P.page_size);
-    int fetch = first;  // unit the cursors stand at
-    int page[2], off[2];
-    auto next_pages = [&]() {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        page[i] = -1;
-        off[i] = cur[i].off;
-        if (fetch < last && fetch * 16 + g + 8 * i < len) {
-          page[i] = table[cur[i].blk];
-          if (page[i] < 0 || page[i] >= P.num_pages) {
-            page[i] = -1;
-            bad_page = true;
-          }
-        }
-        cur[i].advance(P.page_size);
-      }
-      ++fetch;
-    };
-    Unit<CH> unit[DEPTH];
-    auto load_unit = [&](Unit<CH>& x) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const T* row = kbase + page[i] * P.page_stride + off[i] * P.slot_stride;
-#pragma unroll
-        for (int c = 0; c < CH; ++c)
-          x.a[i][c] = page[i] >= 0 ? load_stream(row + c * (64 / sizeof(T)))
-                                   : make_uint4(0u, 0u, 0u, 0u);
-      }
-    };
-    next_pages();
-#pragma unroll
-    for (int i = 0; i < DEPTH; ++i) {
-      load_unit(unit[i]);
-      next_pages();
-    }
-    for (int blk0 = first; blk0 < last; blk0 += DEPTH) {
-#pragma unroll
-      for (int i = 0; i < DEPTH; ++i) {
-        const int blk = blk0 + i;
-        if (blk < last) {
-          float acc[NT][4];
-          sc.scores(unit[i].a, acc, sq);
-          load_unit(unit[i]);
-          next_pages();
-          const int key = blk * 16 + g;
-          bool pass = false;
-#pragma unroll
-          for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const bool live = n * 8 + 2 * t + (e & 1) < heads && key + (e >> 1) * 8 < len;
-              const float z = live ? P.c * acc[n][e] : -INFINITY;
-              acc[n][e] = z;
-              bad[n][e & 1] |= !(z < INFINITY);
-              pass |= z > m[n][e & 1] - 1.f;
-            }
-          if (__any_sync(kFull, pass)) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                float x = fmaxf(acc[n][e], acc[n][2 + e]);
-#pragma unroll
-                for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-                m[n][e] = fmaxf(m[n][e], x);
-#pragma unroll
-                for (int i2 = 0; i2 < 2; ++i2) {
-                  const float z = acc[n][2 * i2 + e];
-                  const bool in = z > m[n][e] - 1.f;
-                  const unsigned mine = __ballot_sync(kFull, in) & (0x11111111u << t);
-                  if (in)
-                    cand[n][e][cnt[n][e] + __popc(mine & ((1u << lane) - 1u))] =
-                        make_int2(__float_as_int(z), key + 8 * i2);
-                  cnt[n][e] += __popc(mine);
-                }
-              }
-          }
-        }
-      }
-    }
-    bad_page = __any_sync(kFull, bad_page);
-    if (bad_page && lane == 0) atomicMax(P.status, ENTMAX_ATTN_ERANGE);
-    int2* part = P.parts + (static_cast<int64_t>(w) + static_cast<int64_t>(b) * HG + hg) *
-                               (8 * NT);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const bool nan =
-            (__ballot_sync(kFull, bad[n][e]) & (0x11111111u << t)) != 0u || bad_page;
-        if (g == 0)
-          part[n * 8 + 2 * t + e] = make_int2(cnt[n][e], __float_as_int(nan ? NAN : m[n][e]));
-      }
+    Scorer<T, D, NT> sc;
+    sc.load_q(P, b, hg, sq);
+    score_run<T, D, NT>(P, sc, sq, b, hg, clamped_len(P, b), first, last,
+                        P.parts + (static_cast<int64_t>(w) + static_cast<int64_t>(b) * HG + hg) *
+                                      (8 * NT));
   }
-}
-
-// max that keeps a NaN of either side
-__device__ __forceinline__ float max_nan(float a, float b) {
-  return (a != a || b != b) ? NAN : fmaxf(a, b);
 }
 
 // One block per (request, query head).
 template <typename T, int D, int BK>
 __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeProblem P) {
-  extern __shared__ __align__(16) char smem[];
-  int* start = reinterpret_cast<int*>(smem);  // [parts of the group + 1]: prefix sums of counts
-  __shared__ float2 list[kJoinWarps][kWarpList];  // (z, key bits), one list per warp
-  __shared__ float sums[2][kJoinWarps][4];
-  __shared__ float red[kJoinWarps];
-  __shared__ int scan_buf[kJoinWarps];
-  __shared__ __align__(16) float oacc[kJoinWarps][D];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ JoinSmem sm;
   const int h = blockIdx.x, b = blockIdx.y;
   const int hk = h / P.G, in_group = h - hk * P.G;
   const int hb = in_group / P.heads_per_block, col = in_group - hb * P.heads_per_block;
-  const int64_t row = static_cast<int64_t>(b) * P.Hq + h;
-  T* out = static_cast<T*>(P.out) + row * D;
-  const int raw_len = P.lens[b];
+  const int raw_len = P.lens[b], len = clamped_len(P, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");
 
-  const int len = clamped_len(P, b);
-  if (len == 0) {  // no key: o = 0 and tau = +inf; a length out of range: NaN
-    const float x = raw_len == 0 ? 0.f : NAN;
-    for (int i = tid; i < D; i += kJoinThreads) store_elem(out, i, x);
-    if (tid == 0) P.tau[row] = raw_len == 0 ? INFINITY : NAN;
+  if (len == 0) {
+    write_empty<T, D>(P, b, h, raw_len == 0);
     return;
   }
   const int HG = P.Hkv * P.head_blocks;
@@ -427,177 +697,11 @@ __global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeP
   const int64_t A = static_cast<int64_t>(P.pre[b]) * HG + static_cast<int64_t>(hg) * nb;
   // the warps whose runs hold the group's first and last unit: the last w with w N / nw <= unit
   const int64_t w0 = ((A + 1) * nw - 1) / N, w1 = ((A + nb) * nw - 1) / N;
-  const int np = static_cast<int>(w1 - w0) + 1;
-  const int2* part = P.parts + (w0 + static_cast<int64_t>(b) * HG + hg) * P.heads_per_block + col;
-
-  float m = -INFINITY;
-  for (int i = tid; i < np; i += kJoinThreads)
-    m = max_nan(m, __int_as_float(part[static_cast<int64_t>(i) * P.heads_per_block].y));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
-  if (lane == 0) red[warp] = m;
-  __syncthreads();
-  m = red[0];
-#pragma unroll
-  for (int i = 1; i < kJoinWarps; ++i) m = max_nan(m, red[i]);
-  if (!(m > -INFINITY)) {  // NaN, or every score -inf: p is not defined
-    for (int i = tid; i < D; i += kJoinThreads) store_elem(out, i, NAN);
-    if (tid == 0) P.tau[row] = NAN;
-    return;
-  }
-  // Candidates of the parts that reach the window, as one sequence of E entries
-  int E = 0;
-  for (int i0 = 0; i0 < np; i0 += kJoinThreads) {
-    const int i = i0 + tid;
-    int n = 0;
-    if (i < np) {
-      const int2 x = part[static_cast<int64_t>(i) * P.heads_per_block];
-      if (__int_as_float(x.y) > m - 1.f) n = x.x;
-    }
-    int total;
-    const int incl = block_scan<kJoinWarps>(n, scan_buf, &total);
-    if (i < np) start[i] = E + incl - n;
-    E += total;
-  }
-  if (tid == 0) start[np] = E;
-  __syncthreads();
-  const int2* cand = P.cand + row * P.cand_stride;
-  auto entry = [&](int e) {  // the e-th candidate: in the last part that starts at or before e
-    int lo = 0, hi = np - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (start[mid] <= e) lo = mid;
-      else hi = mid - 1;
-    }
-    const int64_t u = (w0 + lo) * N / nw;  // the part's first unit
-    const int64_t k0 = u > A ? (u - A) * 16 : 0;
-    return cand[k0 + e - start[lo]];
-  };
-  // Each warp compacts its entries with z > m - 1 into its list, in a fixed order.
-  int n_list = 0;
-  for (int e0 = warp * 32; e0 < E; e0 += kJoinThreads) {
-    const int e = e0 + lane;
-    int2 x = make_int2(__float_as_int(-INFINITY), 0);
-    if (e < E) x = entry(e);
-    const bool in = __int_as_float(x.x) > m - 1.f;
-    const unsigned bal = __ballot_sync(kFull, in);
-    const int at = n_list + __popc(bal & ((1u << lane) - 1u));
-    if (in && at < kWarpList) list[warp][at] = make_float2(__int_as_float(x.x), __int_as_float(x.y));
-    n_list += __popc(bal);
-  }
-  __syncwarp();
-  const bool over = __syncthreads_or(n_list > kWarpList);
-
-  // tau
-  Search sr;
-  sr.init(m, len, P.alpha);
-  for (int it = 0; it < P.n_iter; ++it) {
-    const float tau = sr.tau;
-    float s0 = 0.f, s1 = 0.f, s2 = 0.f;
-    auto add = [&](float z) {
-      const float y = z - tau;
-      if (y > 0.f) {
-        float p0, p1, p2;
-        entmax_powers<BK>(y, P.beta, p0, p1, p2);
-        s0 += p0;
-        s1 += p1;
-        s2 += p2;
-      }
-    };
-    if (!over) {
-      for (int e = lane; e < n_list; e += 32) add(list[warp][e].x);
-    } else {
-      for (int e = tid; e < E; e += kJoinThreads) add(__int_as_float(entry(e).x));
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      s0 += __shfl_xor_sync(kFull, s0, o);
-      s1 += __shfl_xor_sync(kFull, s1, o);
-      s2 += __shfl_xor_sync(kFull, s2, o);
-    }
-    if (lane == 0) {
-      sums[it & 1][warp][0] = s0;
-      sums[it & 1][warp][1] = s1;
-      sums[it & 1][warp][2] = s2;
-    }
-    __syncthreads();  // two buffers: the next step writes the other one
-    s0 = s1 = s2 = 0.f;
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) {
-      s0 += sums[it & 1][i][0];
-      s1 += sums[it & 1][i][1];
-      s2 += sums[it & 1][i][2];
-    }
-    sr.step<BK>(s0, s1, s2, P.beta);
-    if (sr.settled()) break;
-  }
-  const float tau = sr.tau;
-
-  // o: 16-byte chunks of the value rows, D sizeof(T) / 16 lanes per row
-  constexpr int LPR = D * sizeof(T) / 16;  // lanes per value row (8, 16 or 32)
-  constexpr int RPW = 32 / LPR;            // value rows per warp load
-  constexpr int EPL = 16 / sizeof(T);      // elements per lane
-  float o[EPL] = {};
-  const int32_t* table = P.tables + b * P.table_stride;
-  const T* vbase = static_cast<const T*>(P.v) + hk * P.head_stride + (lane % LPR) * EPL;
-  const int n_mine = over ? E : n_list;
-  for (int e0 = over ? warp * 32 : 0; e0 < n_mine; e0 += over ? kJoinThreads : 32) {
-    const int e = e0 + lane;
-    float p = 0.f;
-    int64_t at = 0;
-    if (e < n_mine) {
-      float z;
-      int key;
-      if (over) {
-        const int2 x = entry(e);
-        z = __int_as_float(x.x);
-        key = x.y;
-      } else {
-        z = list[warp][e].x;
-        key = __float_as_int(list[warp][e].y);
-      }
-      p = entmax_p<BK>(z - tau, P.beta);
-      if (p > 0.f) {
-        const int blk = key / P.page_size;
-        at = table[blk] * P.page_stride + (key - blk * P.page_size) * P.slot_stride;
-      }
-    }
-    unsigned live = __ballot_sync(kFull, p > 0.f);
-    while (live) {  // RPW rows at a time: this lane's is the (lane / LPR)-th of the set bits
-      unsigned rest = live;
-      int src = -1;
-#pragma unroll
-      for (int i = 0; i < RPW; ++i) {
-        const int bit = rest ? __ffs(rest) - 1 : -1;
-        if (i == lane / LPR) src = bit;
-        rest &= rest - 1u;
-      }
-      live = rest;
-      const float pw = __shfl_sync(kFull, p, src & 31);
-      const int64_t from = __shfl_sync(kFull, at, src & 31);
-      if (src >= 0) {
-        const uint4 x = load_stream(vbase + from);
-        const T* xv = reinterpret_cast<const T*>(&x);
-#pragma unroll
-        for (int i = 0; i < EPL; ++i) o[i] = fmaf(pw, load_elem(xv, i), o[i]);
-      }
-    }
-  }
-#pragma unroll
-  for (int s = LPR; s < 32; s <<= 1)
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) o[i] += __shfl_xor_sync(kFull, o[i], s);
-  if (lane < LPR)
-#pragma unroll
-    for (int i = 0; i < EPL; ++i) oacc[warp][lane * EPL + i] = o[i];
-  __syncthreads();
-  for (int i = tid; i < D; i += kJoinThreads) {
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) s += oacc[k][i];
-    store_elem(out, i, s);
-  }
-  if (tid == 0) P.tau[row] = tau;
+  const int2* parts = P.parts + (w0 + static_cast<int64_t>(b) * HG + hg) * P.heads_per_block + col;
+  join_head<T, D, BK>(
+      P, sm, b, h, len, static_cast<int>(w1 - w0) + 1,
+      [&](int i) { return parts[static_cast<int64_t>(i) * P.heads_per_block]; },
+      [&](int i) -> int64_t { return i > 0 ? ((w0 + i) * N / nw - A) * 16 : 0; });
 }
 
 template <typename T, int D, int NT>
@@ -605,21 +709,20 @@ cudaError_t launch_scores(const DecodeProblem& P, cudaStream_t s) {
   const size_t smem = (sizeof(T) == 4 ? kScoreWarps * 8 * NT * D * sizeof(float) : 0) +
                       sizeof(int) * (P.B + 1);
   auto kern = decode_scores_kernel<T, D, NT>;
-  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       static_cast<int>(smem));
-  if (e != cudaSuccess) return e;
+  if (smem > 47 * 1024) {
+    const cudaError_t e = cudaFuncSetAttribute(
+        kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+  }
   kern<<<kDecodeScoreWarps / kScoreWarps, kScoreThreads, smem, s>>>(P);
   return cudaGetLastError();
 }
 
 template <typename T, int D, int BK>
 cudaError_t launch_join(const DecodeProblem& P, cudaStream_t s) {
-  // parts of one group: at most one per warp, and at most one per unit
-  const int np = min(kDecodeScoreWarps, (P.max_len + 15) / 16);
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(P.Hq, P.B);
   cfg.blockDim = dim3(kJoinThreads);
-  cfg.dynamicSmemBytes = sizeof(int) * (np + 1);
   cfg.stream = s;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;

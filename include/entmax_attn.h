@@ -326,6 +326,7 @@ size_t entmax_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int max_len);
  *   q: element e of (b, h) at b * q_stride_b + h * q_stride_h + e (strides in elements, multiples of
  *      16 bytes); out [B, Hq, d] contiguous, q's dtype; tau fp32 [B, Hq].
  *   seq_lens int32 [B], at most max_len <= W * page_size.
+ *   n_iter: steps of the tau search for alpha > 2; for alpha <= 2 it runs until tau has settled.
  * A request of length 0 (an unused row of the batch) has out = 0 and tau = +inf.  Only the values
  * of keys with p > 0 are read.  A score that is NaN or +inf makes out and tau of its (request,
  * head) NaN.  A length outside [0, max_len] or a page outside [0, num_pages) makes those of the

@@ -1,4 +1,5 @@
-"""Builds libentmax_attn.so in-tree with nvcc for sm_100a.
+"""Builds libentmax_attn.so in-tree with nvcc for sm_100a, and _paged.so, the Python binding of the
+paged-cache entry points, with the host compiler.
 
     python -m adaptive_sparse_attention_b200.build [--force]
 
@@ -20,6 +21,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libentmax_attn.so")
+BINDING = os.path.join(PKG, "_paged.so")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-Wall",
@@ -77,7 +79,36 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
             sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
             raise RuntimeError("link failed")
         os.replace(tmp, LIB)
+    build_binding(force, verbose)
     return LIB
+
+
+def build_binding(force: bool = False, verbose: bool = False) -> str:
+    """_paged.so: csrc/paged_binding.cpp over torch's C++ tensors, linked to libentmax_attn.so."""
+    src = os.path.join(CSRC, "paged_binding.cpp")
+    if force or _stale(BINDING, [src] + headers() + [__file__]):
+        import sysconfig
+
+        import torch
+        root = os.path.dirname(torch.__file__)
+        cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+        inc = [os.path.join(root, "include"),
+               os.path.join(root, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include"), INCLUDE]
+        tmp = BINDING + f".tmp{os.getpid()}"
+        cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall"]
+        for d in inc:
+            cmd += ["-isystem" if d != INCLUDE else "-I", d]
+        cmd += [src, "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
+                "-ltorch", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:" + os.path.basename(LIB),
+                "-Wl,-rpath,$ORIGIN"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if verbose or r.returncode != 0:
+            sys.stderr.write(" ".join(cmd) + "\n" + r.stdout + r.stderr)
+        if r.returncode != 0:
+            raise RuntimeError("building the paged-cache binding failed")
+        os.replace(tmp, BINDING)
+    return BINDING
 
 
 if __name__ == "__main__":

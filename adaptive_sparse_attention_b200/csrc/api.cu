@@ -501,19 +501,42 @@ size_t decode_layout(void* base, int B, int Hq, int Hkv, int max_len, ea::Decode
   P->score_warps = ea::kDecodeScoreWarps;
   P->cand_stride = (static_cast<int64_t>(max_len) + 15) / 16 * 16;
   const int64_t groups = static_cast<int64_t>(B) * Hkv * P->head_blocks;
-  // unit counts and their sum over the batch are 32-bit on the device
-  if (static_cast<int64_t>(B) * (P->cand_stride / 16) >= (int64_t(1) << 31)) return 0;
+  if (groups > (int64_t(1) << 31)) return 0;
+  // units are numbered in 32 bits on the device, those of the runs past the last one too
+  if (groups * (P->cand_stride / 16) + P->score_warps >= (int64_t(1) << 31)) return 0;
   if (Hq > (1 << 24)) return 0;
   char* p = static_cast<char*>(base);
   size_t off = 0;
   P->pre = reinterpret_cast<int32_t*>(p + off);
   off += align256(sizeof(int32_t) * (static_cast<size_t>(B) + 1));
   P->parts = reinterpret_cast<int2*>(p + off);
-  off += align256(sizeof(int2) * static_cast<size_t>(P->score_warps + groups) *
+  off += align256(sizeof(int2) *
+                  static_cast<size_t>(std::max(groups * 64, P->score_warps + groups)) *
                   P->heads_per_block);
   P->cand = reinterpret_cast<int2*>(p + off);
   off += align256(sizeof(int2) * static_cast<size_t>(B) * Hq * P->cand_stride);
   return off;
+}
+
+// Which of the decode kernels serves a call, from its sizes (times on a B200, bf16, d = 128, Hkv =
+// 8, G = 4, alpha = 1.5 with key spikes, in us; the lengths themselves are on the device only):
+//   cluster: one cluster of 8 blocks per (request, head group), one launch.  Ahead while all
+//     clusters fit in one wave (2 blocks per SM) and a block's share of the keys, which it reads
+//     at about 44 GB/s, is short against the second launch and the prefix sums of the split
+//     kernels (about 5 us) and their 6.2 TB/s.  B = 1: 12.6 against 16.6 at 4096 keys, 20.7
+//     against 20.7 at 16384, 102 against 56 at 131072; B = 4: 28.9 against 35.6 at 16384; B = 16
+//     (four waves): 49 against 36 at 4096.
+//   join_blocks of the split kernels: with up to 148 heads a cluster of 4 blocks each (B = 4, 20000
+//     keys, alpha = 1.333 without spikes: 41 against 48 with one block; the same with few
+//     candidates), with up to 1024 a block each (B = 16, 128 keys: 16.8 against 18.7 with a warp
+//     each), beyond that a warp each (B = 64, 128 keys: 20.6 against 30.9 with a block each).
+void choose_decode_kernels(ea::DecodeProblem* P, double row_bytes) {
+  const int64_t groups = static_cast<int64_t>(P->B) * P->Hkv * P->head_blocks;
+  const double key_us = row_bytes * 1e-3;  // per 1 GB/s
+  const double us = P->max_len * key_us * (1.0 / (8 * 44.0) - groups / 6200.0);
+  P->cluster = groups * 8 <= 2 * 148 && us <= 5.0 ? 1 : 0;
+  const int64_t heads = static_cast<int64_t>(P->B) * P->Hq;
+  P->join_blocks = heads <= 148 ? 4 : heads <= 1024 ? 1 : 0;
 }
 
 // Both passes on the library's cached workspace of (device, stream); flags as the two-pass form.
@@ -758,6 +781,7 @@ int entmax_attn_decode(const void* q, long long q_stride_b, long long q_stride_h
   P.alpha = alpha;
   P.beta = beta;
   P.c = static_cast<float>((a - 1.0) / std::sqrt(static_cast<double>(d)));
+  choose_decode_kernels(&P, static_cast<double>(d * esz));
   const cudaError_t e = ea::launch_decode(P, dtype, d, stream);
   return e == cudaSuccess ? ENTMAX_ATTN_OK : cuda_fail(e);
 }

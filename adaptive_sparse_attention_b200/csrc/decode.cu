@@ -12,7 +12,7 @@
 // traffic is that of the keys alone unless the supports are wide.
 //
 // What bounds it: HBM reads of the keys.  The cache is split in units of 16 keys of one kv head;
-// all units of the batch are dealt to the grid's warps in equal contiguous runs, whatever the
+// all units of the batch are dealt to the grid's warps in contiguous runs of one length, whatever the
 // requests' lengths, so one long request and many ragged ones load the GPU alike, and the lengths
 // are needed on the device only.  A run that crosses from one (request, kv head) to the next is
 // cut there into parts; part (warp w, group g) has the number w + g, which is unique because
@@ -28,10 +28,9 @@ namespace {
 
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kJoinThreads = 256;
-constexpr int kJoinWarps = kJoinThreads / 32;
-constexpr int kWarpList = 256;  // candidates a warp of the join keeps in shared memory
 constexpr int kNewtonSteps = 64;  // a bound that no search reaches
+constexpr int kFew = 128;   // candidates of a head that need no better bound than m - 1
+constexpr int kSolo = 256;  // candidates of a head that one warp takes alone
 constexpr unsigned kFull = 0xffffffffu;
 
 __device__ __forceinline__ int clamped_len(const DecodeProblem& P, int b) {
@@ -79,6 +78,29 @@ __device__ __forceinline__ uint4 load_stream(const void* p) {
   return r;
 }
 
+// The address of this block's shared variable in block `rank` of the cluster.
+__device__ __forceinline__ uint32_t remote(const void* p, int rank) {
+  uint32_t a = static_cast<uint32_t>(__cvta_generic_to_shared(p)), r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(rank));
+  return r;
+}
+
+// max that keeps a NaN of either side
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// An int that compares as the float does, and back.
+__device__ __forceinline__ int ordered(float x) {
+  const int i = __float_as_int(x);
+  return i ^ ((i >> 31) & 0x7fffffff);
+}
+__device__ __forceinline__ float unordered(int i) {
+  return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
+}
+
 // Scores of 16 keys x 8 NT heads.  Lane 4 g + t holds, of key rows g and g + 8, the 16-byte chunks
 // t, t + 4, t + 8, ... (four lanes read 64 contiguous bytes of a row).  bf16: the chunk's four
 // bf16 pairs are the A fragments of two m16n8k16 products whose k index is permuted the same way
@@ -94,8 +116,9 @@ template <int D, int NT>
 struct Scorer<__nv_bfloat16, D, NT> {
   static constexpr int kChunks = D / 32;  // 16-byte chunks per lane and row
   uint32_t bq[NT][kChunks][4];
-  // q of head group hg of request b
-  __device__ __forceinline__ void load_q(const DecodeProblem& P, int b, int hg, float*) {
+  // q of head group hg of request b into registers
+  __device__ __forceinline__ void load_q(const DecodeProblem& P, int b, int hg, float*, int,
+                                         int) {
     const int hk = hg / P.head_blocks, first = (hg - hk * P.head_blocks) * 8 * NT;
     const int heads = P.G - first;
     const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(P.q) + b * P.q_stride_b +
@@ -132,17 +155,17 @@ template <int D, int NT>
 struct Scorer<float, D, NT> {
   static constexpr int kChunks = D / 16;
   int heads_;
-  // q of head group hg of request b into the warp's shared-memory rows [8 NT][D]
-  __device__ __forceinline__ void load_q(const DecodeProblem& P, int b, int hg, float* sq) {
+  // q of head group hg of request b into shared-memory rows [8 NT][D], by thread i of n; the
+  // threads that share the rows synchronise before and after
+  __device__ __forceinline__ void load_q(const DecodeProblem& P, int b, int hg, float* sq, int i,
+                                         int n) {
     const int hk = hg / P.head_blocks, first = (hg - hk * P.head_blocks) * 8 * NT;
     heads_ = min(8 * NT, P.G - first);
     const float* q = static_cast<const float*>(P.q) + b * P.q_stride_b +
                      (hk * P.G + first) * P.q_stride_h;
-    __syncwarp();
-    for (int i = threadIdx.x & 31; i < heads_ * (D / 4); i += 32)
+    for (; i < heads_ * (D / 4); i += n)
       reinterpret_cast<float4*>(sq)[i] = *reinterpret_cast<const float4*>(
           q + (i / (D / 4)) * P.q_stride_h + (i % (D / 4)) * 4);
-    __syncwarp();
   }
   __device__ __forceinline__ void scores(const uint4 (&a)[2][kChunks], float (&acc)[NT][4],
                                          const float* sq) const {
@@ -204,11 +227,15 @@ struct RowCursor {
 
 // One warp scores units [first, last) of 16 keys of head group hg of request b and appends the
 // candidates of each head to the group's lists at the run's first key, a count and a max per head
-// to part.  sq: the warp's (or block's) shared-memory q rows, fp32 only.
-template <typename T, int D, int NT>
+// to part.  sq: the warp's (or block's) shared-memory q rows, fp32 only.  SHARE: the warps of a
+// cluster of 8 blocks, all at the same heads, tell each other the largest score that they have met
+// (known, one copy per block), so that each keeps few candidates beside those of the end: which
+// ones depends on the timing, but the join drops all of them again.
+template <typename T, int D, int NT, bool SHARE>
 __device__ __forceinline__ void score_run(const DecodeProblem& P,
                                           const Scorer<T, D, NT>& sc, const float* sq, int b,
-                                          int hg, int len, int first, int last, int2* part) {
+                                          int hg, int len, int first, int last, int2* part,
+                                          int* known) {
   using S = Scorer<T, D, NT>;
   constexpr int CH = S::kChunks;
   // 8 KB of keys in flight per warp
@@ -220,18 +247,19 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
   const int32_t* table = P.tables + b * P.table_stride;
   const T* kbase = static_cast<const T*>(P.k) + hk * P.head_stride + t * (16 / sizeof(T));
 
-  float m[NT][2];
+  float m[NT][2];     // the largest score known, from which the threshold follows
+  float own[NT][2];   // this lane's largest score; NaN once it has met one
+  float none[NT][2];  // added to the scores: -inf for columns without a head
   int cnt[NT][2];
-  bool bad[NT][2];
   int2* cand[NT][2];
 #pragma unroll
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      m[n][e] = -INFINITY;
+      m[n][e] = own[n][e] = -INFINITY;
       cnt[n][e] = 0;
-      bad[n][e] = false;
       const int h = n * 8 + 2 * t + e;
+      none[n][e] = h < heads ? 0.f : -INFINITY;
       cand[n][e] = P.cand + (static_cast<int64_t>(b) * P.Hq + h0 + min(h, heads - 1)) *
                                 P.cand_stride + first * 16;
     }
@@ -277,6 +305,8 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
     load_unit(unit[i]);
     next_pages();
   }
+  // known is set in every block
+  if (SHARE) asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
   for (int blk0 = first; blk0 < last; blk0 += DEPTH) {
 #pragma unroll
     for (int i = 0; i < DEPTH; ++i) {
@@ -287,18 +317,26 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
         load_unit(unit[i]);
         next_pages();
         const int key = blk * 16 + g;
-        bool pass = false;
+        bool above = false, pass = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const bool live = n * 8 + 2 * t + (e & 1) < heads && key + (e >> 1) * 8 < len;
-            const float z = live ? P.c * acc[n][e] : -INFINITY;
-            acc[n][e] = z;
-            bad[n][e & 1] |= !(z < INFINITY);
-            pass |= z > m[n][e & 1] - 1.f;
+          for (int e = 0; e < 2; ++e) {
+            float z0 = fmaf(P.c, acc[n][e], none[n][e]);
+            float z1 = fmaf(P.c, acc[n][2 + e], none[n][e]);
+            if (key >= len) z0 = -INFINITY;
+            if (key + 8 >= len) z1 = -INFINITY;
+            acc[n][e] = z0;
+            acc[n][2 + e] = z1;
+            own[n][e] = max_nan(own[n][e], max_nan(z0, z1));
+            if (SHARE)
+              m[n][e] = fmaxf(m[n][e],
+                              unordered(*static_cast<volatile int*>(known + n * 8 + 2 * t + e)));
+            const float top = fmaxf(z0, z1);
+            above |= top > m[n][e];
+            pass |= top > m[n][e] - 1.f;
           }
-        if (__any_sync(kFull, pass)) {
+        if (__any_sync(kFull, above)) {  // a new maximum
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -306,7 +344,19 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
               float x = fmaxf(acc[n][e], acc[n][2 + e]);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+              if (SHARE && x > m[n][e])  // lane 4 g + t tells block g
+                asm volatile("red.relaxed.cluster.shared::cluster.max.s32 [%0], %1;" ::"r"(
+                                 remote(known + n * 8 + 2 * t + e, g)),
+                             "r"(ordered(x))
+                             : "memory");
               m[n][e] = fmaxf(m[n][e], x);
+            }
+        }
+        if (__any_sync(kFull, pass)) {  // (with the maximum of before: a superset)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 2; ++e)
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
                 const float z = acc[n][2 * r + e];
@@ -317,7 +367,6 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
                       make_int2(__float_as_int(z), key + 8 * r);
                 cnt[n][e] += __popc(mine);
               }
-            }
         }
       }
     }
@@ -328,171 +377,351 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
   for (int n = 0; n < NT; ++n)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const bool nan = (__ballot_sync(kFull, bad[n][e]) & (0x11111111u << t)) != 0u || bad_page;
-      if (g == 0)
-        part[n * 8 + 2 * t + e] = make_int2(cnt[n][e], __float_as_int(nan ? NAN : m[n][e]));
+      float x = own[n][e];
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1) x = max_nan(x, __shfl_xor_sync(kFull, x, o));
+      if (g == 0)  // NaN also stands for +inf and for a page that does not exist
+        part[n * 8 + 2 * t + e] =
+            make_int2(cnt[n][e], __float_as_int(x < INFINITY && !bad_page ? x : NAN));
     }
-}
-
-// max that keeps a NaN of either side
-__device__ __forceinline__ float max_nan(float a, float b) {
-  return (a != a || b != b) ? NAN : fmaxf(a, b);
 }
 
 // x^beta for x > 0 (or 0 where x <= 0), to a few units of the last place: near beta = 3 the cube
 // times x^(beta - 3), whose exponent is small enough for the fast logarithm's error.
+__device__ __forceinline__ float tiny_power(float x, float f) {  // x^f for |f| <= kNearIntFrac
+  return exp2f(f * __log2f(fmaxf(x, 1e-30f)));
+}
 template <int BK>
 __device__ __forceinline__ float power(float x, float beta) {
   if (!(x > 0.f)) return 0.f;
   if (BK == kBetaOne) return x;
   if (BK == kBetaTwo) return x * x;
-  if (BK == kBetaNear3) return (x * x) * (x * exp2f((beta - 3.f) * __log2f(x)));
+  if (BK == kBetaNear3) return (x * x) * (x * tiny_power(x, beta - 3.f));
   return exp2f(beta * log2f(x));
 }
 
+// Shared memory of a join by C blocks of W warps.
+template <int W, int C = 1>
 struct JoinSmem {
-  float2 list[kJoinWarps][kWarpList];  // (z, key bits): each warp's candidates
-  float2 sums[2][kJoinWarps];
-  float sums2[2][kJoinWarps];
-  float red[kJoinWarps];
-  float2 live[kJoinWarps][32];  // (p, -) and offsets of the values being added
-  int64_t from[kJoinWarps][32];
-  __align__(16) float o[kJoinWarps][128];
+  static constexpr int kList = 256;  // candidates per warp kept here
+  struct Row {
+    int64_t from;  // offset of a value row
+    float p;
+  };
+  union {
+    float2 list[W][kList];  // (z or p, key bits)
+    float o[W][128];        // after the lists: partial sums of o
+  };
+  float2 all[W > 1 ? kSolo : 1];  // all candidates, when they are few
+  Row rows[W][32];
+  float2 sums[2][C * W];
+  float sums2[2][C * W];
+  float red[W];
+  int count[C * W];
+  float co[C > 1 ? C : 1][C > 1 ? 128 : 1];  // the blocks' sums of o
 };
 
-// One block joins the parts of one (request, query head): part(i) is its i-th count and max,
-// key0(i) the first key of part i in the candidate list.
-template <typename T, int D, int BK, typename Part, typename Key0>
-__device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem& sm, int b, int h,
-                                          int len, int np, const Part& part, const Key0& key0) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+// What orders the C W warps of a join.
+template <int W, int C>
+__device__ __forceinline__ void join_sync() {
+  if (C > 1) {
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  } else if (W == 1) {
+    __syncwarp();
+  } else {
+    __syncthreads();
+  }
+}
+
+// Stores to the shared memory of another block.
+__device__ __forceinline__ void store_remote(uint32_t a, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
+}
+__device__ __forceinline__ void store_remote(uint32_t a, int x) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+}
+__device__ __forceinline__ void store_remote(uint32_t a, float2 x) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x.x), "f"(x.y)
+               : "memory");
+}
+// x into *p of every block of the join, by one warp
+template <int C, typename V>
+__device__ __forceinline__ void share(V* p, V x) {
+  const int lane = threadIdx.x & 31;
+  if (C > 1) {
+    if (lane < C) store_remote(remote(p, lane), x);
+  } else if (lane == 0) {
+    *p = x;
+  }
+}
+
+// One step towards tau from the left, for beta >= 1: Newton's on the norm
+// g(tau) = (sum [z - tau]_+^beta)^(1/beta), which is 1 at tau.  g is convex and falling (a norm of
+// functions that are), so from a point where g >= 1 the iterates rise to the root and never pass
+// it, and g is linear in tau while the support stays and the scores tie, so they are few: 4 or 5
+// on normal scores, 14 at most over a wide sweep of sizes and spreads at beta = 1.  With s0, s1
+// the sums of the powers beta and beta - 1, (g - 1) / -g' = (s0 - s0^(1 - 1/beta)) / s1; near the
+// root (s0 - 1) / (beta s1) to first order, which does not cancel.
+template <int BK>
+__device__ __forceinline__ float norm_step(float s0, float s1, float beta) {
+  float rise;
+  if (BK == kBetaOne) rise = s0 - 1.f;
+  else if (s0 < 1.01f) rise = (s0 - 1.f) * (BK == kBetaTwo ? 0.5f : 1.f / beta);
+  else if (BK == kBetaTwo) rise = s0 - s0 * rsqrtf(s0);
+  else rise = s0 - exp2f((1.f - 1.f / beta) * __log2f(s0));
+  return __fdividef(rise, s1);
+}
+// adds x^beta and x^(beta - 1) for x = [z - tau]_+
+template <int BK>
+__device__ __forceinline__ void norm_add(float x, float beta, float& s0, float& s1) {
+  float q;  // x^(beta - 1), 0 at x = 0
+  if (BK == kBetaOne) q = x > 0.f ? 1.f : 0.f;
+  else if (BK == kBetaTwo) q = x;
+  else if (BK == kBetaNear3) q = x * (x * tiny_power(x, beta - 3.f));
+  else q = x > 0.f ? exp2f((beta - 1.f) * log2f(x)) : 0.f;
+  s1 += q;
+  s0 = fmaf(q, x, s0);
+}
+__device__ __forceinline__ void warp_sum2(float& a, float& b) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    a += __shfl_xor_sync(kFull, a, o);
+    b += __shfl_xor_sync(kFull, b, o);
+  }
+}
+
+// From the maxima of a head's parts: its largest score m, and a lower bound of tau.  The maxima
+// are scores of the head, and the tau of a part of the keys is at most that of all (more keys only
+// add to the sum), so a few of the steps above on up to 256 of them give a bound far above m - 1:
+// of 20000 normal scores at alpha = 1.333, 184 lie above tau, 226 above the bound from 64 maxima
+// and 3496 above m - 1 (with few candidates it is m - 1: the steps cost more than they save).
+// Every warp computes both, so that they need no barrier; red: for more
+// than 256 parts, whose maximum the block takes together.
+struct Bounds {
+  float m, floor;
+};
+template <int BK, int W, typename Part>
+__device__ __forceinline__ Bounds part_bounds(const DecodeProblem& P, float* red, int np,
+                                              const Part& part) {
+  constexpr int R = 8;
+  const int lane = threadIdx.x & 31;
+  float x[R];
+  int count[R];
+  Bounds r;
+  r.m = -INFINITY;
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    x[j] = -INFINITY;
+    count[j] = 0;
+    if (lane + 32 * j < np) {
+      const int2 y = part(lane + 32 * j);
+      x[j] = __int_as_float(y.y);
+      count[j] = y.x;
+    }
+    r.m = max_nan(r.m, x[j]);
+  }
+  if (np > 32 * R)
+    for (int i = 32 * R + (W == 1 ? lane : threadIdx.x); i < np; i += 32 * W)
+      r.m = max_nan(r.m, __int_as_float(part(i).y));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) r.m = max_nan(r.m, __shfl_xor_sync(kFull, r.m, o));
+  if (W > 1 && np > 32 * R) {
+    if (lane == 0) red[threadIdx.x >> 5] = r.m;
+    __syncthreads();
+    r.m = red[lane % W];
+#pragma unroll
+    for (int o = W / 2; o > 0; o >>= 1) r.m = max_nan(r.m, __shfl_xor_sync(kFull, r.m, o));
+  }
+  r.floor = r.m - 1.f;
+  int n = 0;  // candidates above m - 1
+#pragma unroll
+  for (int j = 0; j < R; ++j)
+    if (x[j] > r.floor) n += count[j];
+  n = __reduce_add_sync(kFull, n);
+  if (n > kFew && (BK != kBetaGeneral || P.beta >= 1.f)) {
+    for (int it = 0; it < 3; ++it) {
+      float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+        if (32 * j < np) norm_add<BK>(fmaxf(x[j] - r.floor, 0.f), P.beta, s0, s1);
+      warp_sum2(s0, s1);
+      r.floor += norm_step<BK>(s0, s1, P.beta);
+    }
+    r.floor -= 4.f * FLT_EPSILON * (fabsf(r.m) + 1.f);  // the steps' rounding
+    r.floor = fmaxf(r.floor, r.m - 1.f);
+  }
+  return r;
+}
+
+// C blocks (a cluster) of W warps, or one warp of a block for W = 1, join the parts of one
+// (request, query head) with these bounds: part(i) is the i-th part's count and max, key0(i) its
+// first key in the candidate list.
+template <typename T, int D, int BK, int W, int C, typename Part, typename Key0>
+__device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>& sm, int rank,
+                                          int b, int h, int len, int np, Bounds bound,
+                                          const Part& part, const Key0& key0) {
+  constexpr int kThreads = 32 * W;
+  constexpr int kAll = C * W;  // warps of the join
+  constexpr int kList = JoinSmem<W, C>::kList;
+  const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5;
+  const int me = rank * W + warp;
+  const float m = bound.m, floor = bound.floor;
+  const int tid = W == 1 ? lane : threadIdx.x;
   const int hk = h / P.G;
   const int64_t row = static_cast<int64_t>(b) * P.Hq + h;
   T* out = static_cast<T*>(P.out) + row * D;
+  auto undefined = [&]() {
+    if (rank == 0) {
+      for (int i = tid; i < D; i += kThreads) store_elem(out, i, NAN);
+      if (tid == 0) P.tau[row] = NAN;
+    }
+  };
+  if (!(m > -INFINITY)) return undefined();  // a NaN, or every score -inf: p is not defined
 
-  float m = -INFINITY;
-  for (int i = tid; i < np; i += kJoinThreads) m = max_nan(m, __int_as_float(part(i).y));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = max_nan(m, __shfl_xor_sync(kFull, m, o));
-  if (lane == 0) sm.red[warp] = m;
-  __syncthreads();
-  m = sm.red[0];
-#pragma unroll
-  for (int i = 1; i < kJoinWarps; ++i) m = max_nan(m, sm.red[i]);
-  if (!(m > -INFINITY)) {  // NaN, or every score -inf: p is not defined
-    for (int i = tid; i < D; i += kJoinThreads) store_elem(out, i, NAN);
-    if (tid == 0) P.tau[row] = NAN;
-    return;
-  }
-
-  // Each warp compacts the entries with z > m - 1 of a contiguous range of parts, in order: the
-  // first kWarpList into shared memory, the others back to the front of the range (an entry only
-  // moves forward, over entries that the warp has read already).
+  // Each warp compacts the entries above the bound of a contiguous range of parts, in order: the
+  // first kList into shared memory, the others back to the front of the range (an entry only moves
+  // forward, over places that the warp has read already, since it reads them in order).
   int2* cand = P.cand + row * P.cand_stride;
-  const int i_end = static_cast<int>(static_cast<int64_t>(warp + 1) * np / kJoinWarps);
-  const int i_beg = static_cast<int>(static_cast<int64_t>(warp) * np / kJoinWarps);
+  const int i_end = (me + 1) * np / kAll;
+  const int i_beg = me * np / kAll;
   int2* spill = cand + (i_beg < i_end ? key0(i_beg) : 0);
+  const unsigned below = (1u << lane) - 1u;
   int n_list = 0;
   for (int i0 = i_beg; i0 < i_end; i0 += 32) {
-    int n = 0;
-    int64_t k0 = 0;
+    // 32 parts as one sequence of chunks of up to 32 entries: lane i's part owns the chunks from
+    // first on, chunk c of it is at cand[base + 32 c ..), its entries end at 32 c + lane < limit
+    int n = 0, first, base = 0;
     if (i0 + lane < i_end) {
       const int2 x = part(i0 + lane);
-      if (__int_as_float(x.y) > m - 1.f) n = x.x;
-      k0 = key0(i0 + lane);
+      if (__int_as_float(x.y) > floor) n = x.x;
+      base = key0(i0 + lane);
     }
-    int start = n;  // of this lane's part in the sequence of the 32 parts' entries
+    const int chunks = (n + 31) >> 5;
+    first = chunks;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, start, o);
-      if (lane >= o) start += y;
+      const int y = __shfl_up_sync(kFull, first, o);
+      if (lane >= o) first += y;
     }
-    const int total = __shfl_sync(kFull, start, 31);
-    start -= n;
-    const int64_t shift = k0 - start;
-    constexpr int U = 4;  // loads in flight per lane
-    for (int e0 = 0; e0 < total; e0 += 32 * U) {
+    const int total = __shfl_sync(kFull, first, 31);
+    first -= chunks;
+    base -= 32 * first;
+    const int limit = 32 * first + n;
+    constexpr int U = 8;  // loads in flight per lane
+    for (int c0 = 0; c0 < total; c0 += U) {
       int2 x[U];
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int e = e0 + 32 * j + lane;
-        int lo = 0;  // the last part that starts at or before e
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1)
-          if (__shfl_sync(kFull, start, lo + o) <= e) lo += o;
-        const int64_t at = __shfl_sync(kFull, shift, lo) + e;
+        const int c = c0 + j;
+        // its part is the last that starts at or before it (a part without chunks starts where
+        // the next one does)
+        const int own = 31 - __clz(__ballot_sync(kFull, first <= c));
+        const int at = __shfl_sync(kFull, base, own) + 32 * c + lane;
+        const int end = __shfl_sync(kFull, limit, own);
         x[j] = make_int2(__float_as_int(-INFINITY), 0);
-        if (e < total) x[j] = cand[at];
+        if (c < total && 32 * c + lane < end) x[j] = cand[at];
       }
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const bool in = __int_as_float(x[j].x) > m - 1.f;
+        const bool in = __int_as_float(x[j].x) > floor;
         const unsigned bal = __ballot_sync(kFull, in);
-        const int at = n_list + __popc(bal & ((1u << lane) - 1u));
+        const int at = n_list + __popc(bal & below);
         if (in) {
-          if (at < kWarpList)
+          if (at < kList)
             sm.list[warp][at] = make_float2(__int_as_float(x[j].x), __int_as_float(x[j].y));
           else
-            spill[at - kWarpList] = x[j];
+            spill[at - kList] = x[j];
         }
         n_list += __popc(bal);
       }
     }
   }
+  // When the candidates are few, the first warp takes them all and finds tau and the p by itself,
+  // with no sum over the warps or blocks per step, and deals the values to add to its block's
+  // warps.
+  bool solo = W == 1;
+  if (W > 1) {
+    share<C>(&sm.count[me], n_list);
+    join_sync<W, C>();
+    // inclusive scan of the counts, lane l holding those of warps K l .. K l + K - 1
+    constexpr int K = kAll > 32 ? kAll / 32 : 1;
+    int x = 0;
+#pragma unroll
+    for (int i = 0; i < K; ++i)
+      if (K * lane + i < kAll) x += sm.count[K * lane + i];
+    const int own = x;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    const int total = __shfl_sync(kFull, x, 31);
+    if (total <= kSolo) {
+      int at = __shfl_sync(kFull, x - own, me / K);
+      for (int i = 0; i < me % K; ++i) at += sm.count[me / K * K + i];
+      for (int e = lane; e < n_list; e += 32) {  // n_list <= kSolo <= kList
+        if (C > 1) store_remote(remote(&sm.all[at + e], 0), sm.list[warp][e]);
+        else sm.all[at + e] = sm.list[warp][e];
+      }
+      n_list = total;
+      solo = true;
+      join_sync<W, C>();
+      if (C > 1 && rank != 0) return;
+    }
+  }
   __syncwarp();
+  if (solo && n_list == 0) return undefined();  // |m| >= 2^23: m - 1 is m in fp32
+  const bool deal = W > 1 && solo;
+  float2* list = deal ? sm.all : sm.list[warp];
   auto entry = [&](int e) {
-    if (e < kWarpList) return sm.list[warp][e];
-    const int2 x = spill[e - kWarpList];
+    if (e < kList) return list[e];  // all of them when solo: kSolo <= kList
+    const int2 x = spill[e - kList];
     return make_float2(__int_as_float(x.x), __int_as_float(x.y));
   };
+  auto set_entry = [&](int e, float z, int key) {
+    if (e < kList) list[e] = make_float2(z, __int_as_float(key));
+    else spill[e - kList] = make_int2(__float_as_int(z), key);
+  };
 
-  // tau.  For beta >= 1 by Newton's steps on the norm g(tau) = (sum [z - tau]_+^beta)^(1/beta) = 1
-  // from tau = m - 1, where g >= 1: g is convex and falling (a norm of functions that are), so
-  // the iterates rise to the root and never pass it, and it is linear in tau while the support
-  // stays and the scores tie, so the steps are few: with S0, S1 the sums of the powers beta and
-  // beta - 1, (g - 1) / -g' = (S0 - S0^(1 - 1/beta)) / S1.  They run until tau has settled (4 or 5
-  // steps on normal scores, 14 at most over a wide sweep of sizes and spreads at beta = 1), so
-  // n_iter does not enter.  For beta < 1 g is not convex, and the bracketed search of the
-  // attention passes is used.
-  float tau;
-  if (BK != kBetaGeneral || P.beta >= 1.f) {
-    tau = m - 1.f;
+  // tau: for beta >= 1 by the steps of norm_step from the lower bound, until it has settled
+  // (n_iter does not enter); for beta < 1, where the norm is not convex, by the bracketed search
+  // of the attention passes.
+  float tau = 0.f;
+  if (deal && warp != 0) {
+    // waits for the first warp below
+  } else if (BK != kBetaGeneral || P.beta >= 1.f) {
+    tau = floor;
     for (int it = 0; it < kNewtonSteps; ++it) {
       float s0 = 0.f, s1 = 0.f;
-      for (int e = lane; e < n_list; e += 32) {
-        const float y = entry(e).x - tau;
-        if (BK == kBetaOne) {
-          if (y > 0.f) {
-            s0 += y;
-            s1 += 1.f;
-          }
-        } else if (BK == kBetaTwo) {
-          const float x = fmaxf(y, 0.f);
-          s1 += x;
-          s0 = fmaf(x, x, s0);
-        } else if (y > 0.f) {
-          const float p = power<BK>(y, P.beta);
-          s0 += p;
-          s1 += __fdividef(p, y);
+      for (int e0 = lane; e0 < n_list; e0 += 128) {
+        float x[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int e = e0 + 32 * j;
+          x[j] = e < n_list ? fmaxf(entry(e).x - tau, 0.f) : 0.f;
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) norm_add<BK>(x[j], P.beta, s0, s1);
+      }
+      warp_sum2(s0, s1);
+      if (W > 1 && !solo) {
+        share<C>(&sm.sums[it & 1][me], make_float2(s0, s1));
+        join_sync<W, C>();  // two buffers: the next step writes the other one
+        s0 = s1 = 0.f;
+#pragma unroll
+        for (int i = lane % kAll; i < kAll; i += 32) {
+          const float2 x = sm.sums[it & 1][i];
+          s0 += x.x;
+          s1 += x.y;
+        }
+#pragma unroll
+        for (int o = (kAll < 32 ? kAll : 32) / 2; o > 0; o >>= 1) {
+          s0 += __shfl_xor_sync(kFull, s0, o);
+          s1 += __shfl_xor_sync(kFull, s1, o);
         }
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        s0 += __shfl_xor_sync(kFull, s0, o);
-        s1 += __shfl_xor_sync(kFull, s1, o);
-      }
-      if (lane == 0) sm.sums[it & 1][warp] = make_float2(s0, s1);
-      __syncthreads();  // two buffers: the next step writes the other one
-      s0 = s1 = 0.f;
-#pragma unroll
-      for (int i = 0; i < kJoinWarps; ++i) {
-        s0 += sm.sums[it & 1][i].x;
-        s1 += sm.sums[it & 1][i].y;
-      }
-      float step;
-      if (BK == kBetaOne) step = (s0 - 1.f) / s1;
-      else if (BK == kBetaTwo) step = (s0 - sqrtf(s0)) / s1;
-      else step = (s0 - exp2f((1.f - 1.f / P.beta) * log2f(s0))) / s1;
+      const float step = norm_step<BK>(s0, s1, P.beta);
       tau += step;
       if (!(step > 2.f * FLT_EPSILON * fmaxf(fabsf(tau), m - tau))) break;
     }
@@ -517,17 +746,16 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem& sm, 
         s1 += __shfl_xor_sync(kFull, s1, o);
         s2 += __shfl_xor_sync(kFull, s2, o);
       }
-      if (lane == 0) {
-        sm.sums[it & 1][warp] = make_float2(s0, s1);
-        sm.sums2[it & 1][warp] = s2;
-      }
-      __syncthreads();
-      s0 = s1 = s2 = 0.f;
-#pragma unroll
-      for (int i = 0; i < kJoinWarps; ++i) {
-        s0 += sm.sums[it & 1][i].x;
-        s1 += sm.sums[it & 1][i].y;
-        s2 += sm.sums2[it & 1][i];
+      if (W > 1 && !solo) {
+        share<C>(&sm.sums[it & 1][me], make_float2(s0, s1));
+        share<C>(&sm.sums2[it & 1][me], s2);
+        join_sync<W, C>();
+        s0 = s1 = s2 = 0.f;
+        for (int i = 0; i < kAll; ++i) {
+          s0 += sm.sums[it & 1][i].x;
+          s1 += sm.sums[it & 1][i].y;
+          s2 += sm.sums2[it & 1][i];
+        }
       }
       sr.step<BK>(s0, s1, s2, P.beta);
       if (sr.settled()) break;
@@ -535,8 +763,33 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem& sm, 
     tau = sr.tau;
   }
 
-  // o: each warp adds the values of its entries with p > 0, in 16-byte chunks, D sizeof(T) / 16
-  // lanes per row, four rows per lane group in flight
+  // The entries with p > 0 move to the front of the list, p in the place of z ...
+  int n_live = 0;
+  if (!deal || warp == 0) {
+    for (int e0 = 0; e0 < n_list; e0 += 32) {
+      float p = 0.f;
+      int key = 0;
+      if (e0 + lane < n_list) {
+        const float2 x = entry(e0 + lane);
+        p = power<BK>(x.x - tau, P.beta);
+        key = __float_as_int(x.y);
+      }
+      const unsigned live = __ballot_sync(kFull, p > 0.f);
+      if (p > 0.f) set_entry(n_live + __popc(live & below), p, key);
+      n_live += __popc(live);
+    }
+    if (deal && lane == 0) sm.count[0] = n_live;
+  }
+  if (deal) {
+    __syncthreads();
+    n_live = sm.count[0];
+  } else {
+    __syncwarp();
+  }
+  const int step = deal ? W : 1, mine = deal ? warp : 0;  // this warp's entries: mine + i step
+  n_live = (n_live - mine + step - 1) / step;
+  // ... and their values are added in 16-byte chunks, D sizeof(T) / 16 lanes per row, four rows
+  // per lane group in flight.
   constexpr int LPR = D * sizeof(T) / 16;  // lanes per value row (8, 16 or 32)
   constexpr int RPW = 32 / LPR;            // value rows per warp load
   constexpr int EPL = 16 / sizeof(T);      // elements per lane
@@ -544,22 +797,14 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem& sm, 
   float o[EPL] = {};
   const int32_t* table = P.tables + b * P.table_stride;
   const T* vbase = static_cast<const T*>(P.v) + hk * P.head_stride + (lane % LPR) * EPL;
-  for (int e0 = 0; e0 < n_list; e0 += 32) {
-    float p = 0.f;
-    int key = 0;
-    if (e0 + lane < n_list) {
-      const float2 x = entry(e0 + lane);
-      p = power<BK>(x.x - tau, P.beta);
-      key = __float_as_int(x.y);
-    }
-    const unsigned live = __ballot_sync(kFull, p > 0.f);
-    if (!live) continue;
-    const int n = __popc(live);
-    if (p > 0.f) {
-      const int at = __popc(live & ((1u << lane) - 1u));
-      const int blk = key / P.page_size;
-      sm.live[warp][at].x = p;
-      sm.from[warp][at] = table[blk] * P.page_stride + (key - blk * P.page_size) * P.slot_stride;
+  for (int e0 = 0; e0 < n_live; e0 += 32) {
+    const int n = min(32, n_live - e0);
+    if (lane < n) {
+      const float2 x = entry(mine + (e0 + lane) * step);
+      const int key = __float_as_int(x.y), blk = key / P.page_size;
+      sm.rows[warp][lane].p = x.x;
+      sm.rows[warp][lane].from =
+          table[blk] * P.page_stride + (key - blk * P.page_size) * P.slot_stride;
     }
     __syncwarp();
     for (int i0 = 0; i0 < n; i0 += RPW * U) {
@@ -571,8 +816,8 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem& sm, 
         w[j] = 0.f;
         x[j] = make_uint4(0u, 0u, 0u, 0u);
         if (i < n) {
-          w[j] = sm.live[warp][i].x;
-          x[j] = load_stream(vbase + sm.from[warp][i]);
+          w[j] = sm.rows[warp][i].p;
+          x[j] = load_stream(vbase + sm.rows[warp][i].from);
         }
       }
 #pragma unroll
@@ -588,26 +833,39 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem& sm, 
   for (int s = LPR; s < 32; s <<= 1)
 #pragma unroll
     for (int i = 0; i < EPL; ++i) o[i] += __shfl_xor_sync(kFull, o[i], s);
+  join_sync<W, 1>();  // the lists are no longer needed
   if (lane < LPR)
 #pragma unroll
     for (int i = 0; i < EPL; ++i) sm.o[warp][lane * EPL + i] = o[i];
-  __syncthreads();
-  for (int i = tid; i < D; i += kJoinThreads) {
+  join_sync<W, 1>();
+  for (int i = tid; i < D; i += kThreads) {
     float s = 0.f;
 #pragma unroll
-    for (int k = 0; k < kJoinWarps; ++k) s += sm.o[k][i];
-    store_elem(out, i, s);
+    for (int k = 0; k < W; ++k) s += sm.o[k][i];
+    if (C > 1 && !solo) store_remote(remote(&sm.co[rank][i], 0), s);
+    else store_elem(out, i, s);
   }
-  if (tid == 0) P.tau[row] = tau;
+  if (C > 1 && !solo) {
+    join_sync<W, C>();
+    if (rank == 0)
+      for (int i = tid; i < D; i += kThreads) {
+        float s = 0.f;
+#pragma unroll
+        for (int k = 0; k < C; ++k) s += sm.co[k][i];
+        store_elem(out, i, s);
+      }
+  }
+  if (rank == 0 && tid == 0) P.tau[row] = tau;
 }
 
 // o and tau of a request without keys (o = 0, tau = +inf) or with a length out of range (NaN)
 template <typename T, int D>
-__device__ __forceinline__ void write_empty(const DecodeProblem& P, int b, int h, bool valid) {
+__device__ __forceinline__ void write_empty(const DecodeProblem& P, int b, int h, bool valid,
+                                            int tid, int threads) {
   const int64_t row = static_cast<int64_t>(b) * P.Hq + h;
   T* out = static_cast<T*>(P.out) + row * D;
-  for (int i = threadIdx.x; i < D; i += kJoinThreads) store_elem(out, i, valid ? 0.f : NAN);
-  if (threadIdx.x == 0) P.tau[row] = valid ? INFINITY : NAN;
+  for (int i = tid; i < D; i += threads) store_elem(out, i, valid ? 0.f : NAN);
+  if (tid == 0) P.tau[row] = valid ? INFINITY : NAN;
 }
 
 // ------------------------------------------------------------------ split: two kernels --
@@ -642,18 +900,17 @@ __global__ void __launch_bounds__(kScoreThreads, 4) decode_scores_kernel(const D
       if (P.lens[b] < 0 || P.lens[b] > P.max_len) atomicMax(P.status, ENTMAX_ATTN_ERANGE);
   }
   const int HG = P.Hkv * P.head_blocks;  // groups per request
-  const int64_t N = static_cast<int64_t>(pre[P.B]) * HG;
-  const int64_t nw = min(static_cast<int64_t>(gridDim.x) * kScoreWarps, N);
+  const int N = pre[P.B] * HG;           // below 2^31, see decode_layout
+  const int run = (N + P.score_warps - 1) / P.score_warps;
   const int w = blockIdx.x * kScoreWarps + warp;
-  if (w >= nw) return;
-  int64_t u = w * N / nw;
-  const int64_t u_end = (w + 1) * N / nw;
+  int u = w * run;  // at most score_warps more than N
+  const int u_end = min(u + run, N);
   float* sq = sq_all + warp * 8 * NT * D;
 
   while (u < u_end) {
     // the request of unit u: the last b with pre[b] <= u / HG (empty requests have pre[b + 1] =
     // pre[b] and are never last)
-    const int v = static_cast<int>(u / HG);
+    const int v = u / HG;
     int lo = 0, hi = P.B - 1;
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
@@ -662,46 +919,139 @@ __global__ void __launch_bounds__(kScoreThreads, 4) decode_scores_kernel(const D
     }
     const int b = lo;
     const int nb = pre[b + 1] - pre[b];
-    const int64_t r = u - static_cast<int64_t>(pre[b]) * HG;
-    const int hg = static_cast<int>(r / nb);
-    const int first = static_cast<int>(r - static_cast<int64_t>(hg) * nb);
-    const int last = static_cast<int>(min(static_cast<int64_t>(nb), first + (u_end - u)));
+    const int r = u - pre[b] * HG;
+    const int hg = r / nb;
+    const int first = r - hg * nb;
+    const int last = min(nb, first + (u_end - u));
     u += last - first;
     Scorer<T, D, NT> sc;
-    sc.load_q(P, b, hg, sq);
-    score_run<T, D, NT>(P, sc, sq, b, hg, clamped_len(P, b), first, last,
-                        P.parts + (static_cast<int64_t>(w) + static_cast<int64_t>(b) * HG + hg) *
-                                      (8 * NT));
+    __syncwarp();
+    sc.load_q(P, b, hg, sq, tid & 31, 32);
+    __syncwarp();
+    score_run<T, D, NT, false>(
+        P, sc, sq, b, hg, clamped_len(P, b), first, last,
+        P.parts + (static_cast<int64_t>(w) + static_cast<int64_t>(b) * HG + hg) * (8 * NT),
+        nullptr);
   }
 }
 
-// One block per (request, query head).
-template <typename T, int D, int BK>
-__global__ void __launch_bounds__(kJoinThreads) decode_join_kernel(const DecodeProblem P) {
-  __shared__ JoinSmem sm;
-  const int h = blockIdx.x, b = blockIdx.y;
-  const int hk = h / P.G, in_group = h - hk * P.G;
-  const int hb = in_group / P.heads_per_block, col = in_group - hb * P.heads_per_block;
+// The parts of one (request, query head) in the score kernel's numbering.
+struct SplitParts {
+  const int2* parts;
+  int run, w0, A, stride, np;
+  __device__ __forceinline__ SplitParts(const DecodeProblem& P, int b, int h, int len) {
+    const int hk = h / P.G, in_group = h - hk * P.G;
+    const int hb = in_group / P.heads_per_block, col = in_group - hb * P.heads_per_block;
+    const int HG = P.Hkv * P.head_blocks;
+    run = (P.pre[P.B] * HG + P.score_warps - 1) / P.score_warps;
+    const int nb = (len + 15) >> 4;
+    const int hg = hk * P.head_blocks + hb;
+    A = P.pre[b] * HG + hg * nb;  // the group's first unit
+    w0 = A / run;
+    np = (A + nb - 1) / run - w0 + 1;
+    stride = P.heads_per_block;
+    parts = P.parts + (static_cast<int64_t>(w0) + static_cast<int64_t>(b) * HG + hg) * stride +
+            col;
+  }
+  __device__ __forceinline__ int2 part(int i) const {
+    return parts[static_cast<int64_t>(i) * stride];
+  }
+  __device__ __forceinline__ int key0(int i) const { return i > 0 ? ((w0 + i) * run - A) * 16 : 0; }
+};
+
+// A cluster of C blocks of 8 warps per (request, query head).
+constexpr int kJoinWarps = 8;
+template <typename T, int D, int BK, int C>
+__global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const DecodeProblem P) {
+  __shared__ JoinSmem<kJoinWarps, C> sm;
+  const int rank = C > 1 ? blockIdx.x : 0;
+  const int h = blockIdx.y, b = blockIdx.z;
   const int raw_len = P.lens[b], len = clamped_len(P, b);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-
   if (len == 0) {
-    write_empty<T, D>(P, b, h, raw_len == 0);
+    if (rank == 0) write_empty<T, D>(P, b, h, raw_len == 0, threadIdx.x, 32 * kJoinWarps);
     return;
   }
-  const int HG = P.Hkv * P.head_blocks;
-  const int64_t N = static_cast<int64_t>(P.pre[P.B]) * HG;
-  const int64_t nw = min(static_cast<int64_t>(P.score_warps), N);
-  const int nb = (len + 15) >> 4;
-  const int hg = hk * P.head_blocks + hb;
-  const int64_t A = static_cast<int64_t>(P.pre[b]) * HG + static_cast<int64_t>(hg) * nb;
-  // the warps whose runs hold the group's first and last unit: the last w with w N / nw <= unit
-  const int64_t w0 = ((A + 1) * nw - 1) / N, w1 = ((A + nb) * nw - 1) / N;
-  const int2* parts = P.parts + (w0 + static_cast<int64_t>(b) * HG + hg) * P.heads_per_block + col;
-  join_head<T, D, BK>(
-      P, sm, b, h, len, static_cast<int>(w1 - w0) + 1,
-      [&](int i) { return parts[static_cast<int64_t>(i) * P.heads_per_block]; },
-      [&](int i) -> int64_t { return i > 0 ? ((w0 + i) * N / nw - A) * 16 : 0; });
+  if (C > 1) {  // every block runs before any stores into its shared memory
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  }
+  const SplitParts sp(P, b, h, len);
+  auto part = [&](int i) { return sp.part(i); };
+  const Bounds bound = part_bounds<BK, kJoinWarps>(P, sm.red, sp.np, part);
+  if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
+  join_head<T, D, BK, kJoinWarps, C>(P, sm, rank, b, h, len, sp.np, bound, part,
+                                     [&](int i) { return sp.key0(i); });
+}
+
+// Many heads: one warp per (request, query head), eight to a block; a head with more than
+// kWarpEntries candidates is left to the whole block.
+constexpr int kHeadWarps = 8;
+constexpr int kWarpEntries = 768;
+
+template <typename T, int D, int BK>
+__global__ void __launch_bounds__(32 * kHeadWarps) decode_join_many_kernel(const DecodeProblem P) {
+  __shared__ union {
+    JoinSmem<kHeadWarps> block;
+    JoinSmem<1> warp[kHeadWarps];
+  } sm;
+  __shared__ Bounds heavy_bound[kHeadWarps];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int64_t rows = static_cast<int64_t>(P.B) * P.Hq;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kHeadWarps;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  bool heavy = false;
+  if (row0 + warp < rows) {
+    const int b = static_cast<int>((row0 + warp) / P.Hq);
+    const int h = static_cast<int>(row0 + warp - static_cast<int64_t>(b) * P.Hq);
+    const int raw_len = P.lens[b], len = clamped_len(P, b);
+    if (len == 0) {
+      write_empty<T, D>(P, b, h, raw_len == 0, lane, 32);
+    } else {
+      const SplitParts sp(P, b, h, len);
+      auto part = [&](int i) { return sp.part(i); };
+      const Bounds bound = part_bounds<BK, 1>(P, nullptr, sp.np, part);
+      int n = 0;
+      for (int i = lane; i < sp.np; i += 32) {
+        const int2 x = part(i);
+        if (__int_as_float(x.y) > bound.floor) n += x.x;
+      }
+      n = __reduce_add_sync(kFull, n);
+      heavy = n > kWarpEntries;
+      if (lane == 0) heavy_bound[warp] = bound;
+      if (!heavy)
+        join_head<T, D, BK, 1, 1>(P, sm.warp[warp], 0, b, h, len, sp.np, bound, part,
+                                  [&](int i) { return sp.key0(i); });
+    }
+  }
+  __shared__ int heavy_warps;
+  if (tid == 0) heavy_warps = 0;
+  __syncthreads();
+  if (heavy && lane == 0) atomicOr(&heavy_warps, 1 << warp);
+  __syncthreads();
+  const int todo = heavy_warps;
+  if (__popc(todo) >= kHeadWarps / 2) {  // as fast a warp each as one after the other
+    if (heavy) {
+      const int b = static_cast<int>((row0 + warp) / P.Hq);
+      const int h = static_cast<int>(row0 + warp - static_cast<int64_t>(b) * P.Hq);
+      const int len = clamped_len(P, b);
+      const SplitParts sp(P, b, h, len);
+      join_head<T, D, BK, 1, 1>(P, sm.warp[warp], 0, b, h, len, sp.np, heavy_bound[warp],
+                                [&](int i) { return sp.part(i); },
+                                [&](int i) { return sp.key0(i); });
+    }
+    return;
+  }
+  for (int left = todo; left; left &= left - 1) {
+    const int w = __ffs(left) - 1;
+    const int b = static_cast<int>((row0 + w) / P.Hq);
+    const int h = static_cast<int>(row0 + w - static_cast<int64_t>(b) * P.Hq);
+    const int len = clamped_len(P, b);
+    const SplitParts sp(P, b, h, len);
+    join_head<T, D, BK, kHeadWarps, 1>(P, sm.block, 0, b, h, len, sp.np, heavy_bound[w],
+                                       [&](int i) { return sp.part(i); },
+                                       [&](int i) { return sp.key0(i); });
+    __syncthreads();  // shared memory of this head
+  }
 }
 
 template <typename T, int D, int NT>
@@ -718,30 +1068,122 @@ cudaError_t launch_scores(const DecodeProblem& P, cudaStream_t s) {
   return cudaGetLastError();
 }
 
+// The join after the score kernel, launched while it runs (griddepcontrol.wait holds it back).
 template <typename T, int D, int BK>
 cudaError_t launch_join(const DecodeProblem& P, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(P.Hq, P.B);
-  cfg.blockDim = dim3(kJoinThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = P.join_blocks;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = P.join_blocks > 1 ? 2 : 1;
+  if (P.join_blocks == 0) {
+    const int64_t rows = static_cast<int64_t>(P.B) * P.Hq;
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + kHeadWarps - 1) / kHeadWarps));
+    cfg.blockDim = dim3(32 * kHeadWarps);
+    return cudaLaunchKernelEx(&cfg, decode_join_many_kernel<T, D, BK>, P);
+  }
+  cfg.gridDim = dim3(P.join_blocks, P.Hq, P.B);
+  cfg.blockDim = dim3(32 * kJoinWarps);
+  switch (P.join_blocks) {
+    case 4: return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, BK, 4>, P);
+    default: return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, BK, 1>, P);
+  }
+}
+
+// ------------------------------------------------------------------ cluster: one kernel --
+
+constexpr int kClusterBlocks = 8;
+constexpr int kClusterWarps = 8;  // per block
+constexpr int kClusterParts = kClusterBlocks * kClusterWarps;
+
+// A cluster of 8 blocks scores one (request, head group), each of its 64 warps an equal run of
+// units, and after a cluster barrier its blocks join the group's heads.  One launch and no prefix
+// sums: less latency than the split kernels, which only the batch's longest requests repay.
+template <typename T, int D, int NT, int BK>
+__global__ void __launch_bounds__(32 * kClusterWarps, 2)
+    decode_cluster_kernel(const DecodeProblem P) {
+  __shared__ JoinSmem<kClusterWarps> sm;
+  __shared__ __align__(16) float sq[sizeof(T) == 4 ? 8 * NT * D : 4];
+  __shared__ int known[8 * NT];  // ordered(): the largest score of each head in the cluster so far
+  const int tid = threadIdx.x, warp = tid >> 5;
+  const int rank = blockIdx.x;  // the cluster is the x extent of the grid
+  const int hg = blockIdx.y, b = blockIdx.z;
+  const int HG = P.Hkv * P.head_blocks;
+  if (tid < 8 * NT) known[tid] = ordered(-INFINITY);
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  const int raw_len = P.lens[b], len = clamped_len(P, b);
+  const int nb = (len + 15) >> 4, run = (nb + kClusterParts - 1) / kClusterParts;
+  int2* parts = P.parts + (static_cast<int64_t>(b) * HG + hg) * kClusterParts * (8 * NT);
+  if (len > 0) {
+    Scorer<T, D, NT> sc;
+    sc.load_q(P, b, hg, sq, tid, 32 * kClusterWarps);
+    if (sizeof(T) == 4) __syncthreads();
+    const int part = rank * kClusterWarps + warp;
+    score_run<T, D, NT, true>(P, sc, sq, b, hg, len, min(part * run, nb),
+                              min(part * run + run, nb), parts + part * (8 * NT), known);
+  } else {
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    if (raw_len != 0 && rank == 0 && hg == 0 && tid == 0)
+      atomicMax(P.status, ENTMAX_ATTN_ERANGE);
+  }
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  const int hk = hg / P.head_blocks, hb = hg - hk * P.head_blocks;
+  const int h0 = hk * P.G + hb * 8 * NT, heads = min(8 * NT, P.G - hb * 8 * NT);
+  for (int col = rank; col < heads; col += kClusterBlocks) {
+    if (len == 0) {
+      write_empty<T, D>(P, b, h0 + col, raw_len == 0, tid, 32 * kClusterWarps);
+      continue;
+    }
+    __syncthreads();  // shared memory of the previous head
+    auto part = [&](int i) { return parts[i * (8 * NT) + col]; };
+    const Bounds bound = part_bounds<BK, kClusterWarps>(P, sm.red, kClusterParts, part);
+    join_head<T, D, BK, kClusterWarps, 1>(
+        P, sm, 0, b, h0 + col, len, kClusterParts, bound, part,
+        [&](int i) { return min(i * run, nb) * 16; });
+  }
+}
+
+template <typename T, int D, int NT, int BK>
+cudaError_t launch_cluster(const DecodeProblem& P, cudaStream_t s) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kClusterBlocks, P.Hkv * P.head_blocks, P.B);
+  cfg.blockDim = dim3(32 * kClusterWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = kClusterBlocks;
+  attr.val.clusterDim.y = 1;
+  attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, BK>, P);
+  return cudaLaunchKernelEx(&cfg, decode_cluster_kernel<T, D, NT, BK>, P);
+}
+
+template <typename T, int D, int BK>
+cudaError_t launch_decode_k(const DecodeProblem& P, cudaStream_t s) {
+  if (P.cluster)
+    return P.heads_per_block == 8 ? launch_cluster<T, D, 1, BK>(P, s)
+                                  : launch_cluster<T, D, 2, BK>(P, s);
+  const cudaError_t e = P.heads_per_block == 8 ? launch_scores<T, D, 1>(P, s)
+                                               : launch_scores<T, D, 2>(P, s);
+  if (e != cudaSuccess) return e;
+  return launch_join<T, D, BK>(P, s);
 }
 
 template <typename T, int D>
 cudaError_t launch_decode_t(const DecodeProblem& P, cudaStream_t s) {
-  cudaError_t e = P.heads_per_block == 8 ? launch_scores<T, D, 1>(P, s)
-                                         : launch_scores<T, D, 2>(P, s);
-  if (e != cudaSuccess) return e;
   switch (beta_kind(P.beta)) {
-    case kBetaOne: return launch_join<T, D, kBetaOne>(P, s);
-    case kBetaTwo: return launch_join<T, D, kBetaTwo>(P, s);
-    case kBetaNear3: return launch_join<T, D, kBetaNear3>(P, s);
-    default: return launch_join<T, D, kBetaGeneral>(P, s);
+    case kBetaOne: return launch_decode_k<T, D, kBetaOne>(P, s);
+    case kBetaTwo: return launch_decode_k<T, D, kBetaTwo>(P, s);
+    case kBetaNear3: return launch_decode_k<T, D, kBetaNear3>(P, s);
+    default: return launch_decode_k<T, D, kBetaGeneral>(P, s);
   }
 }
 

@@ -690,7 +690,7 @@ int entmax_attn_paged_append(const void* k, const void* v, long long stride_b, l
                              long long page_stride, long long head_stride, long long slot_stride,
                              int num_pages, int page_size, const int64_t* slots, int B, int Hkv,
                              int T, int d, int dtype, cudaStream_t stream) {
-  if (!k || !v || !slots || B < 1 || Hkv < 1 || T < 1 ||
+  if (!k || !v || !slots || B < 1 || Hkv < 1 || Hkv > 65535 || T < 1 ||
       static_cast<int64_t>(B) * T >= (int64_t(1) << 31) || stride_b < 0 || stride_h < 0 ||
       stride_t < 0)
     return ENTMAX_ATTN_EINVAL;

@@ -167,32 +167,46 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
   }
 }
 
-// One 16-byte vector of one (token, kv head) row of k or v per thread and step; a row's vectors
-// are consecutive lanes.  A pure copy: bound by HBM.
+// The copies of one chunk of tokens: a block takes kTokens tokens of one kv head of k or v, VPR
+// threads per row of VPR 16-byte vectors, U rows in flight per thread.  A pure copy: bound by HBM.
+// The rows of consecutive tokens are consecutive in a [Hkv, N, d] input and, within a page, in a
+// [pages, Hkv, page_size, d] cache.  The grid is (chunks of tokens, kv heads, k or v), so that no
+// index needs a 64-bit division.
+constexpr int kAppendThreads = 256;
+constexpr int kAppendRows = 4;  // rows per thread
 template <int VPR>  // 16-byte vectors per row
-__global__ void __launch_bounds__(256) paged_append_kernel(const PagedAppend P) {
-  const int64_t rows = static_cast<int64_t>(P.n_tokens) * P.Hkv;
-  const int64_t per_grid = static_cast<int64_t>(gridDim.x) * (256 / VPR);
+__global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const PagedAppend P) {
+  constexpr int kStep = kAppendThreads / VPR;
   const int lane = threadIdx.x % VPR;
-  const char* src = static_cast<const char*>(blockIdx.y ? P.v : P.k) + lane * 16;
-  char* dst = static_cast<char*>(blockIdx.y ? P.v_cache : P.k_cache) + lane * 16;
-  for (int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / VPR) + threadIdx.x / VPR; r < rows;
-       r += per_grid) {
-    const int h = static_cast<int>(r / P.n_tokens);
-    const int n = static_cast<int>(r - static_cast<int64_t>(h) * P.n_tokens);
-    const int64_t slot = P.slots[n];
-    if (slot < 0) continue;  // a padding row
-    if (slot >= P.n_slots) {
+  const int h = blockIdx.y;
+  const char* src = static_cast<const char*>(blockIdx.z ? P.v : P.k) + lane * 16 +
+                    h * P.stride_h;
+  char* dst = static_cast<char*>(blockIdx.z ? P.v_cache : P.k_cache) + lane * 16 +
+              h * P.head_stride;
+  const int n0 = blockIdx.x * (kStep * kAppendRows) + threadIdx.x / VPR;
+  int64_t slot[kAppendRows];
+  uint4 x[kAppendRows];
+#pragma unroll
+  for (int i = 0; i < kAppendRows; ++i) {
+    const int n = n0 + i * kStep;
+    slot[i] = n < P.n_tokens ? P.slots[n] : -1;
+    const int b = P.T == P.n_tokens ? 0 : n / P.T, t = n - b * P.T;
+    if (n < P.n_tokens)
+      x[i] = *reinterpret_cast<const uint4*>(src + b * P.stride_b + t * P.stride_t);
+  }
+#pragma unroll
+  for (int i = 0; i < kAppendRows; ++i) {
+    if (slot[i] < 0) continue;  // a padding row
+    if (slot[i] >= P.n_slots) {
       if (lane == 0) atomicMax(P.status, ENTMAX_ATTN_ERANGE);
       continue;
     }
-    const int b = n / P.T, t = n - b * P.T;
-    const int64_t page = slot / P.page_size;
-    const int off = static_cast<int>(slot - page * P.page_size);
-    const uint4 x = *reinterpret_cast<const uint4*>(src + b * P.stride_b + h * P.stride_h +
-                                                    t * P.stride_t);
-    *reinterpret_cast<uint4*>(dst + page * P.page_stride + h * P.head_stride +
-                              off * P.slot_stride) = x;
+    // num_pages and page_size are ints, so the page of a valid slot is too
+    int64_t page;
+    if (P.n_slots <= 0x7fffffff) page = static_cast<int>(slot[i]) / P.page_size;
+    else page = slot[i] / P.page_size;
+    const int off = static_cast<int>(slot[i] - page * P.page_size);
+    *reinterpret_cast<uint4*>(dst + page * P.page_stride + off * P.slot_stride) = x[i];
   }
 }
 
@@ -214,13 +228,13 @@ cudaError_t launch_page_tables(const PageTables& P, cudaStream_t s) {
 
 cudaError_t launch_paged_append(const PagedAppend& P, int row_bytes, cudaStream_t s) {
   const int vpr = row_bytes / 16;
-  const int64_t rows = static_cast<int64_t>(P.n_tokens) * P.Hkv;
-  const int64_t want = (rows * vpr + 255) / 256;
-  const dim3 grid(static_cast<unsigned>(want > 148 * 8 ? 148 * 8 : want), 2);
+  const int per_block = kAppendThreads / vpr * kAppendRows;
+  const dim3 grid(static_cast<unsigned>((P.n_tokens - 1) / per_block + 1),
+                  static_cast<unsigned>(P.Hkv), 2);
   switch (vpr) {
-    case 8: paged_append_kernel<8><<<grid, 256, 0, s>>>(P); break;
-    case 16: paged_append_kernel<16><<<grid, 256, 0, s>>>(P); break;
-    default: paged_append_kernel<32><<<grid, 256, 0, s>>>(P);
+    case 8: paged_append_kernel<8><<<grid, kAppendThreads, 0, s>>>(P); break;
+    case 16: paged_append_kernel<16><<<grid, kAppendThreads, 0, s>>>(P); break;
+    default: paged_append_kernel<32><<<grid, kAppendThreads, 0, s>>>(P);
   }
   return cudaGetLastError();
 }

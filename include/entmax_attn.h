@@ -309,7 +309,7 @@ int entmax_attn_page_tables(const int32_t* lens, const int32_t* new_lens,
  * status word.  The slots of one call must differ (of a slot given twice, either token's row or a
  * mixture of both is stored).  dtype ENTMAX_ATTN_FP32 or ENTMAX_ATTN_BF16 throughout; d 64 or 128.
  * Device pointers, 16-byte aligned (slots 8); asynchronous on `stream`.  Returns ENTMAX_ATTN_OK,
- * ENTMAX_ATTN_EINVAL (null pointer, size < 1, B * T >= 2^31, bad d, dtype or stride) ,
+ * ENTMAX_ATTN_EINVAL (null pointer, size < 1, B * T >= 2^31, Hkv > 65535, bad d, dtype or stride),
  * ENTMAX_ATTN_EALIGN or ENTMAX_ATTN_ECUDA. */
 int entmax_attn_paged_append(const void* k, const void* v, long long stride_b, long long stride_h,
                              long long stride_t, void* k_cache, void* v_cache,

@@ -9,6 +9,7 @@ namespace {
 
 constexpr int kTableThreads = 512;
 constexpr int kTableWarps = kTableThreads / 32;
+constexpr int kSlots = 4;  // consecutive slots per thread, one search for all
 constexpr unsigned kFull = 0xffffffffu;
 
 struct Grow {
@@ -58,12 +59,20 @@ __device__ __forceinline__ void scan2(int& x, int& y, int2* buf, int& tx, int& t
   y += by;
 }
 
-// last b with a[b] <= v (a nondecreasing, a[0] <= v)
-__device__ __forceinline__ int last_at_most(const int* a, int n, int v) {
+// A request as the blocks look it up.
+struct Entry {
+  int token;  // its first new token
+  int page;   // its first entry of the free list, counted from free_start
+  int len;    // tokens held, -1 if it is not served
+  int have;   // pages held
+};
+// last b with e[b].FIELD <= v (nondecreasing, e[0].FIELD <= v)
+template <int Entry::*FIELD>
+__device__ __forceinline__ int last_at_most(const Entry* e, int n, int v) {
   int lo = 0, hi = n - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
-    if (a[mid] <= v) lo = mid;
+    if (e[mid].*FIELD <= v) lo = mid;
     else hi = mid - 1;
   }
   return lo;
@@ -71,12 +80,11 @@ __device__ __forceinline__ int last_at_most(const int* a, int n, int v) {
 
 // Every block scans the B lengths itself (a few KB from L2, no second launch and no order between
 // blocks), then writes its share of the new table entries and of the slots.  Bound by the launch
-// and the two dependent loads for small batches, by the slots' writes (8 bytes a token) for large
-// ones.
+// and three dependent loads for small batches (64 requests of one token: 5 us), by the search and
+// the writes of 8 bytes a token for large ones.
 __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTables P) {
-  extern __shared__ int smem[];
-  int* cu = smem;             // [B + 1] first new token of each request
-  int* page0 = smem + P.B + 1;  // [B + 1] first free-list entry of each request, from free_start
+  extern __shared__ __align__(16) char smem[];
+  Entry* req = reinterpret_cast<Entry*>(smem);  // [B + 1], the last holds the totals
   __shared__ int2 buf[kTableWarps];
   __shared__ int served_pages;
   const int tid = threadIdx.x;
@@ -98,72 +106,82 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
     y -= pages;
     for (int b = b0; b < b1; ++b) {
       const Grow r = grow_of(P, b);
-      cu[b] = x;
-      page0[b] = y;
-      x += r.add;
-      y += r.need - r.have;
+      const int x1 = x + r.add, y1 = y + r.need - r.have;
+      // A request is served if its lengths fit, its tokens lie inside the slots and its pages
+      // inside the free list.  Requests that take pages are served in order until the list is
+      // exhausted.
+      const bool ok = r.ok && (P.padded || x1 <= P.n_new) && (r.need == r.have || y1 <= avail);
+      req[b] = {x, y, ok ? P.lens[b] : -1, r.have};
+      x = x1;
+      y = y1;
     }
-    if (tid == 0) {
-      cu[P.B] = tx;
-      page0[P.B] = ty;
-    }
+    if (tid == 0) req[P.B] = {tx, ty, -1, 0};
     __syncthreads();
   }
-  // A request is served if its lengths fit, its tokens lie inside the slots and its pages inside
-  // the free list.  Requests that take pages are served in order until the list is exhausted.
-  auto served = [&](int b, const Grow& r) {
-    return r.ok && (P.padded || cu[b + 1] <= P.n_new) &&
-           (r.need == r.have || page0[b + 1] <= avail);
-  };
+  const int step = gridDim.x * kTableThreads;  // at most 148 blocks
+  const int me = blockIdx.x * kTableThreads + tid;
+  // slots
+  const int64_t n_slots = P.padded ? static_cast<int64_t>(P.B) * P.n_new : P.n_new;
+  for (int64_t i0 = static_cast<int64_t>(me) * kSlots; i0 < n_slots;
+       i0 += static_cast<int64_t>(step) * kSlots) {
+    int b, t;  // of slot i0
+    if (!P.padded) {
+      b = last_at_most<&Entry::token>(req, P.B, static_cast<int>(i0));
+      t = static_cast<int>(i0) - req[b].token;
+    } else if (n_slots <= 0x7fffffff) {
+      b = static_cast<int>(i0) / P.n_new;
+      t = static_cast<int>(i0) - b * P.n_new;
+    } else {
+      b = static_cast<int>(i0 / P.n_new);
+      t = static_cast<int>(i0 - static_cast<int64_t>(b) * P.n_new);
+    }
+    Entry r = req[b];
+    int add = req[b + 1].token - r.token;
+    int64_t slot[kSlots];
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j, ++t) {
+      // on to the request of slot i0 + j: the next one with a new token, or the next row
+      while (t >= (P.padded ? P.n_new : add) && b + 1 < P.B) {
+        r = req[++b];
+        add = req[b + 1].token - r.token;
+        t = 0;
+      }
+      slot[j] = -1;
+      if (r.len >= 0 && t < add) {
+        const int pos = r.len + t;
+        const int blk = pos / P.page_size;
+        const int page = blk < r.have ? P.tables[b * P.table_stride + blk]
+                                      : P.free_pages[start + r.page + (blk - r.have)];
+        if (page >= 0)
+          slot[j] = static_cast<int64_t>(page) * P.page_size + (pos - blk * P.page_size);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < kSlots; ++j)
+      if (i0 + j < n_slots) P.slots[i0 + j] = slot[j];
+  }
+  // new table entries
+  const int n_pages = min(req[P.B].page, avail);
+  for (int j = me; j < n_pages; j += step) {
+    const int b = last_at_most<&Entry::page>(req, P.B, j);
+    const Entry r = req[b];
+    if (r.len >= 0)
+      P.tables[b * P.table_stride + r.have + (j - r.page)] = P.free_pages[start + j];
+  }
   if (blockIdx.x == 0) {
     int most = 0;
     for (int b = tid; b < P.B; b += kTableThreads) {
-      const Grow r = grow_of(P, b);
-      const bool s = served(b, r);
-      P.lens_out[b] = P.lens[b] + (s ? r.add : 0);
-      P.cu_new[b] = cu[b];
-      if (s && r.need > r.have) most = max(most, page0[b + 1]);
+      const Entry r = req[b], next = req[b + 1];
+      P.lens_out[b] = r.len >= 0 ? r.len + (next.token - r.token) : P.lens[b];
+      P.cu_new[b] = r.token;
+      if (r.len >= 0 && next.page > r.page) most = max(most, next.page);
     }
-    atomicMax(&served_pages, most);  // the order does not matter to a maximum
+    if (most) atomicMax(&served_pages, most);  // a maximum does not depend on the order
     __syncthreads();
     if (tid == 0) {
-      P.cu_new[P.B] = cu[P.B];
+      P.cu_new[P.B] = req[P.B].token;
       *P.free_next = start + served_pages;
     }
-  }
-  const int64_t step = static_cast<int64_t>(gridDim.x) * kTableThreads;
-  const int64_t me = static_cast<int64_t>(blockIdx.x) * kTableThreads + tid;
-  // new table entries
-  const int n_pages = min(page0[P.B], avail);
-  for (int64_t j = me; j < n_pages; j += step) {
-    const int b = last_at_most(page0, P.B, static_cast<int>(j));
-    const Grow r = grow_of(P, b);
-    if (served(b, r))
-      P.tables[b * P.table_stride + r.have + (static_cast<int>(j) - page0[b])] =
-          P.free_pages[start + j];
-  }
-  // slots
-  const int64_t n_slots = P.padded ? static_cast<int64_t>(P.B) * P.n_new : P.n_new;
-  for (int64_t i = me; i < n_slots; i += step) {
-    int b, t;
-    if (P.padded) {
-      b = static_cast<int>(i / P.n_new);
-      t = static_cast<int>(i - static_cast<int64_t>(b) * P.n_new);
-    } else {
-      b = last_at_most(cu, P.B, static_cast<int>(i));
-      t = static_cast<int>(i) - cu[b];
-    }
-    const Grow r = grow_of(P, b);
-    int64_t slot = -1;
-    if (t < r.add && served(b, r)) {
-      const int pos = P.lens[b] + t;
-      const int blk = pos / P.page_size;
-      const int page = blk < r.have ? P.tables[b * P.table_stride + blk]
-                                    : P.free_pages[start + page0[b] + (blk - r.have)];
-      if (page >= 0)
-        slot = static_cast<int64_t>(page) * P.page_size + (pos - blk * P.page_size);
-    }
-    P.slots[i] = slot;
   }
 }
 
@@ -214,9 +232,9 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
 
 cudaError_t launch_page_tables(const PageTables& P, cudaStream_t s) {
   const int64_t n_slots = P.padded ? static_cast<int64_t>(P.B) * P.n_new : P.n_new;
-  const int64_t want = (n_slots + kTableThreads - 1) / kTableThreads;
+  const int64_t want = (n_slots - 1) / (kTableThreads * kSlots) + 1;
   const int grid = static_cast<int>(want < 1 ? 1 : want > 148 ? 148 : want);
-  const size_t smem = 2 * sizeof(int) * (P.B + 1);
+  const size_t smem = sizeof(Entry) * (P.B + 1);
   if (smem > 48 * 1024) {
     const cudaError_t e = cudaFuncSetAttribute(
         page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));

@@ -518,23 +518,30 @@ size_t decode_layout(void* base, int B, int Hq, int Hkv, int max_len, ea::Decode
   return off;
 }
 
-// Which of the decode kernels serves a call, from its sizes (times on a B200, bf16, d = 128, Hkv =
-// 8, G = 4, alpha = 1.5 with key spikes, in us; the lengths themselves are on the device only):
-//   cluster: one cluster of 8 blocks per (request, head group), one launch.  Ahead while all
-//     clusters fit in one wave (2 blocks per SM) and a block's share of the keys, which it reads
-//     at about 44 GB/s, is short against the second launch and the prefix sums of the split
-//     kernels (about 5 us) and their 6.2 TB/s.  B = 1: 12.6 against 16.6 at 4096 keys, 20.7
-//     against 20.7 at 16384, 102 against 56 at 131072; B = 4: 28.9 against 35.6 at 16384; B = 16
-//     (four waves): 49 against 36 at 4096.
-//   join_blocks of the split kernels: with up to 148 heads a cluster of 4 blocks each (B = 4, 20000
-//     keys, alpha = 1.333 without spikes: 41 against 48 with one block; the same with few
-//     candidates), with up to 1024 a block each (B = 16, 128 keys: 16.8 against 18.7 with a warp
-//     each), beyond that a warp each (B = 64, 128 keys: 20.6 against 30.9 with a block each).
+// Which of the decode kernels serves a call, from its sizes alone (the lengths are on the device).
+// Times on a B200 in us, bf16, d = 128, Hkv = 8, G = 4, alpha = 1.5 with key spikes, all lengths
+// equal unless said otherwise.
+//   cluster: C = 8, 4, 2 or 1 blocks per (request, head group), the most that run all at once (2
+//     blocks per SM).  One launch, about 5 us ahead of the split kernels (B = 1, 1000 keys: 10.4
+//     against 14.5; B = 16, 128 keys: 12.5 against 16.7; 4096 keys: 31 against 37), but a block
+//     reads about 44 GB/s, so a request much longer than the others, or alone, is late: 1 request of
+//     131072 keys takes 105 against 56.  So they serve a single request as long as its blocks' extra
+//     time against the 6.3 TB/s of the split kernels is below those 5 us, and a batch if its longest
+//     possible request is read in 12 us.
+//   join_blocks of the split kernels: up to 148 heads have a cluster of 4 blocks each (B = 4, lengths
+//     to 20000, alpha = 1.333 without spikes: 42 against 45 with one block), up to 1024 a block each
+//     (B = 16, 128 keys: 16.7 against 18.6 with a warp each), more a warp each (B = 64, 128 keys:
+//     20.7 against 31.2 with a block each).
 void choose_decode_kernels(ea::DecodeProblem* P, double row_bytes) {
   const int64_t groups = static_cast<int64_t>(P->B) * P->Hkv * P->head_blocks;
-  const double key_us = row_bytes * 1e-3;  // per 1 GB/s
-  const double us = P->max_len * key_us * (1.0 / (8 * 44.0) - groups / 6200.0);
-  P->cluster = groups * 8 <= 2 * 148 && us <= 5.0 ? 1 : 0;
+  P->cluster = 0;
+  if (groups <= 2 * 148) {
+    int c = 8;
+    while (groups * c > 2 * 148) c /= 2;
+    const double bytes = P->max_len * row_bytes;  // of the longest request and one kv head
+    const double block_us = bytes / (c * 44e3);
+    if (P->B == 1 ? block_us - groups * bytes / 6300e3 <= 5.0 : block_us <= 12.0) P->cluster = c;
+  }
   const int64_t heads = static_cast<int64_t>(P->B) * P->Hq;
   P->join_blocks = heads <= 148 ? 4 : heads <= 1024 ? 1 : 0;
 }

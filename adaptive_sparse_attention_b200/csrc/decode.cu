@@ -19,6 +19,8 @@
 // every cut advances w or g.
 #include <cuda_bf16.h>
 
+#include <atomic>
+
 #include "common.cuh"
 #include "entmax_attn.h"
 #include "kernels.h"
@@ -227,18 +229,19 @@ struct RowCursor {
 
 // One warp scores units [first, last) of 16 keys of head group hg of request b and appends the
 // candidates of each head to the group's lists at the run's first key, a count and a max per head
-// to part.  sq: the warp's (or block's) shared-memory q rows, fp32 only.  SHARE: the warps of a
-// cluster of 8 blocks, all at the same heads, tell each other the largest score that they have met
-// (known, one copy per block), so that each keeps few candidates beside those of the end: which
-// ones depends on the timing, but the join drops all of them again.
+// to part.  sq: the warp's (or block's) shared-memory q rows, fp32 only.  SHARE: the warps of a cluster of `blocks` blocks, all at the
+// same heads, tell each other the largest score that they have met (known, one copy per block), so
+// that each keeps few candidates beside those of the end: which ones depends on the timing, but the
+// join drops all of them again.
 template <typename T, int D, int NT, bool SHARE>
 __device__ __forceinline__ void score_run(const DecodeProblem& P,
-                                          const Scorer<T, D, NT>& sc, const float* sq, int b,
-                                          int hg, int len, int first, int last, int2* part,
-                                          int* known) {
+                                          const Scorer<T, D, NT>& sc, const float* sq, int b, int hg, int len, int first,
+                                          int last, int2* part, int* known, int blocks) {
   using S = Scorer<T, D, NT>;
   constexpr int CH = S::kChunks;
-  // 8 KB of keys in flight per warp
+  // 8 KB of keys in flight per warp, in registers: 128 KB per SM with 16 warps, which reads at 6.2
+  // TB/s.  (Asynchronous copies into 12 KB of shared memory per warp were slower: 64 requests of
+  // 16384 tokens 445 against 342 us.)
   constexpr int DEPTH = 8192 / (16 * D * static_cast<int>(sizeof(T)));
   const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int hk = hg / P.head_blocks, hb = hg - hk * P.head_blocks;
@@ -344,7 +347,7 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
               float x = fmaxf(acc[n][e], acc[n][2 + e]);
 #pragma unroll
               for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-              if (SHARE && x > m[n][e])  // lane 4 g + t tells block g
+              if (SHARE && x > m[n][e] && g < blocks)  // lane 4 g + t tells block g
                 asm volatile("red.relaxed.cluster.shared::cluster.max.s32 [%0], %1;" ::"r"(
                                  remote(known + n * 8 + 2 * t + e, g)),
                              "r"(ordered(x))
@@ -491,6 +494,17 @@ __device__ __forceinline__ void warp_sum2(float& a, float& b) {
   }
 }
 
+// The parts of one (request, query head): part i holds the candidates of the keys from key0(i) on.
+struct Parts {
+  const int2* info;  // (count, max bits) of part 0
+  int stride, np;    // of info; number of parts
+  int run, off, nb;  // part i starts at unit i run - off of the nb units of the request
+  __device__ __forceinline__ int2 part(int i) const {
+    return info[static_cast<int64_t>(i) * stride];
+  }
+  __device__ __forceinline__ int key0(int i) const { return min(max(i * run - off, 0), nb) * 16; }
+};
+
 // From the maxima of a head's parts: its largest score m, and a lower bound of tau.  The maxima
 // are scores of the head, and the tau of a part of the keys is at most that of all (more keys only
 // add to the sum), so a few of the steps above on up to 256 of them give a bound far above m - 1:
@@ -501,9 +515,10 @@ __device__ __forceinline__ void warp_sum2(float& a, float& b) {
 struct Bounds {
   float m, floor;
 };
-template <int BK, int W, typename Part>
-__device__ __forceinline__ Bounds part_bounds(const DecodeProblem& P, float* red, int np,
-                                              const Part& part) {
+template <int BK, int W>
+__device__ __forceinline__ Bounds part_bounds(const DecodeProblem& P, float* red,
+                                              const Parts& parts) {
+  const int np = parts.np;
   constexpr int R = 8;
   const int lane = threadIdx.x & 31;
   float x[R];
@@ -515,7 +530,7 @@ __device__ __forceinline__ Bounds part_bounds(const DecodeProblem& P, float* red
     x[j] = -INFINITY;
     count[j] = 0;
     if (lane + 32 * j < np) {
-      const int2 y = part(lane + 32 * j);
+      const int2 y = parts.part(lane + 32 * j);
       x[j] = __int_as_float(y.y);
       count[j] = y.x;
     }
@@ -523,7 +538,7 @@ __device__ __forceinline__ Bounds part_bounds(const DecodeProblem& P, float* red
   }
   if (np > 32 * R)
     for (int i = 32 * R + (W == 1 ? lane : threadIdx.x); i < np; i += 32 * W)
-      r.m = max_nan(r.m, __int_as_float(part(i).y));
+      r.m = max_nan(r.m, __int_as_float(parts.part(i).y));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) r.m = max_nan(r.m, __shfl_xor_sync(kFull, r.m, o));
   if (W > 1 && np > 32 * R) {
@@ -555,12 +570,12 @@ __device__ __forceinline__ Bounds part_bounds(const DecodeProblem& P, float* red
 }
 
 // C blocks (a cluster) of W warps, or one warp of a block for W = 1, join the parts of one
-// (request, query head) with these bounds: part(i) is the i-th part's count and max, key0(i) its
-// first key in the candidate list.
-template <typename T, int D, int BK, int W, int C, typename Part, typename Key0>
+// (request, query head) with these bounds.
+template <typename T, int D, int BK, int W, int C>
 __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>& sm, int rank,
-                                          int b, int h, int len, int np, Bounds bound,
-                                          const Part& part, const Key0& key0) {
+                                          int b, int h, int len, Bounds bound,
+                                          const Parts& parts) {
+  const int np = parts.np;
   constexpr int kThreads = 32 * W;
   constexpr int kAll = C * W;  // warps of the join
   constexpr int kList = JoinSmem<W, C>::kList;
@@ -585,7 +600,7 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
   int2* cand = P.cand + row * P.cand_stride;
   const int i_end = (me + 1) * np / kAll;
   const int i_beg = me * np / kAll;
-  int2* spill = cand + (i_beg < i_end ? key0(i_beg) : 0);
+  int2* spill = cand + (i_beg < i_end ? parts.key0(i_beg) : 0);
   const unsigned below = (1u << lane) - 1u;
   int n_list = 0;
   for (int i0 = i_beg; i0 < i_end; i0 += 32) {
@@ -593,9 +608,9 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
     // first on, chunk c of it is at cand[base + 32 c ..), its entries end at 32 c + lane < limit
     int n = 0, first, base = 0;
     if (i0 + lane < i_end) {
-      const int2 x = part(i0 + lane);
+      const int2 x = parts.part(i0 + lane);
       if (__int_as_float(x.y) > floor) n = x.x;
-      base = key0(i0 + lane);
+      base = parts.key0(i0 + lane);
     }
     const int chunks = (n + 31) >> 5;
     first = chunks;
@@ -931,33 +946,27 @@ __global__ void __launch_bounds__(kScoreThreads, 4) decode_scores_kernel(const D
     score_run<T, D, NT, false>(
         P, sc, sq, b, hg, clamped_len(P, b), first, last,
         P.parts + (static_cast<int64_t>(w) + static_cast<int64_t>(b) * HG + hg) * (8 * NT),
-        nullptr);
+        nullptr, 1);
   }
 }
 
 // The parts of one (request, query head) in the score kernel's numbering.
-struct SplitParts {
-  const int2* parts;
-  int run, w0, A, stride, np;
-  __device__ __forceinline__ SplitParts(const DecodeProblem& P, int b, int h, int len) {
-    const int hk = h / P.G, in_group = h - hk * P.G;
-    const int hb = in_group / P.heads_per_block, col = in_group - hb * P.heads_per_block;
-    const int HG = P.Hkv * P.head_blocks;
-    run = (P.pre[P.B] * HG + P.score_warps - 1) / P.score_warps;
-    const int nb = (len + 15) >> 4;
-    const int hg = hk * P.head_blocks + hb;
-    A = P.pre[b] * HG + hg * nb;  // the group's first unit
-    w0 = A / run;
-    np = (A + nb - 1) / run - w0 + 1;
-    stride = P.heads_per_block;
-    parts = P.parts + (static_cast<int64_t>(w0) + static_cast<int64_t>(b) * HG + hg) * stride +
-            col;
-  }
-  __device__ __forceinline__ int2 part(int i) const {
-    return parts[static_cast<int64_t>(i) * stride];
-  }
-  __device__ __forceinline__ int key0(int i) const { return i > 0 ? ((w0 + i) * run - A) * 16 : 0; }
-};
+__device__ __forceinline__ Parts split_parts(const DecodeProblem& P, int b, int h, int len) {
+  const int hk = h / P.G, in_group = h - hk * P.G;
+  const int hb = in_group / P.heads_per_block, col = in_group - hb * P.heads_per_block;
+  const int HG = P.Hkv * P.head_blocks, hg = hk * P.head_blocks + hb;
+  Parts r;
+  r.run = (P.pre[P.B] * HG + P.score_warps - 1) / P.score_warps;
+  r.nb = (len + 15) >> 4;
+  const int A = P.pre[b] * HG + hg * r.nb;  // the group's first unit
+  const int w0 = A / r.run;
+  r.off = A - w0 * r.run;
+  r.np = (A + r.nb - 1) / r.run - w0 + 1;
+  r.stride = P.heads_per_block;
+  r.info = P.parts + (static_cast<int64_t>(w0) + static_cast<int64_t>(b) * HG + hg) * r.stride +
+           col;
+  return r;
+}
 
 // A cluster of C blocks of 8 warps per (request, query head).
 constexpr int kJoinWarps = 8;
@@ -972,98 +981,123 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
     if (rank == 0) write_empty<T, D>(P, b, h, raw_len == 0, threadIdx.x, 32 * kJoinWarps);
     return;
   }
-  if (C > 1) {  // every block runs before any stores into its shared memory
-    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
-  }
-  const SplitParts sp(P, b, h, len);
-  auto part = [&](int i) { return sp.part(i); };
-  const Bounds bound = part_bounds<BK, kJoinWarps>(P, sm.red, sp.np, part);
+  // every block runs before any stores into its shared memory
+  if (C > 1) asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+  const Parts parts = split_parts(P, b, h, len);
+  const Bounds bound = part_bounds<BK, kJoinWarps>(P, sm.red, parts);
   if (C > 1) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
-  join_head<T, D, BK, kJoinWarps, C>(P, sm, rank, b, h, len, sp.np, bound, part,
-                                     [&](int i) { return sp.key0(i); });
+  join_head<T, D, BK, kJoinWarps, C>(P, sm, rank, b, h, len, bound, parts);
 }
 
-// Many heads: one warp per (request, query head), eight to a block; a head with more than
-// kWarpEntries candidates is left to the whole block.
-constexpr int kHeadWarps = 8;
+// One warp per head, up to eight heads to a block; a head with more than kWarpEntries candidates
+// is left to the whole block, unless half of the warps have one.
 constexpr int kWarpEntries = 768;
-
-template <typename T, int D, int BK>
-__global__ void __launch_bounds__(32 * kHeadWarps) decode_join_many_kernel(const DecodeProblem P) {
-  __shared__ union {
-    JoinSmem<kHeadWarps> block;
-    JoinSmem<1> warp[kHeadWarps];
-  } sm;
-  __shared__ Bounds heavy_bound[kHeadWarps];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t rows = static_cast<int64_t>(P.B) * P.Hq;
-  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kHeadWarps;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  bool heavy = false;
-  if (row0 + warp < rows) {
-    const int b = static_cast<int>((row0 + warp) / P.Hq);
-    const int h = static_cast<int>(row0 + warp - static_cast<int64_t>(b) * P.Hq);
-    const int raw_len = P.lens[b], len = clamped_len(P, b);
-    if (len == 0) {
-      write_empty<T, D>(P, b, h, raw_len == 0, lane, 32);
-    } else {
-      const SplitParts sp(P, b, h, len);
-      auto part = [&](int i) { return sp.part(i); };
-      const Bounds bound = part_bounds<BK, 1>(P, nullptr, sp.np, part);
-      int n = 0;
-      for (int i = lane; i < sp.np; i += 32) {
-        const int2 x = part(i);
-        if (__int_as_float(x.y) > bound.floor) n += x.x;
+struct ManySmem {
+  union {
+    JoinSmem<kJoinWarps> block;
+    JoinSmem<1> warp[kJoinWarps];
+  };
+  Bounds bound[kJoinWarps];
+  int heavy;
+};
+// Head(w) gives the b, h, length and parts of warp w's head; valid: this warp has one.
+struct HeadRef {
+  int b, h, len;
+  Parts parts;
+};
+template <typename T, int D, int BK, typename Head>
+__device__ __forceinline__ void join_many(const DecodeProblem& P, ManySmem& sm, bool valid,
+                                          const Head& head) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  if (threadIdx.x == 0) sm.heavy = 0;
+  __syncthreads();
+  if (valid) {
+    const HeadRef r = head(warp);
+    const Bounds bound = part_bounds<BK, 1>(P, nullptr, r.parts);
+    int n = 0;
+    for (int i = lane; i < r.parts.np; i += 32) {
+      const int2 x = r.parts.part(i);
+      if (__int_as_float(x.y) > bound.floor) n += x.x;
+    }
+    n = __reduce_add_sync(kFull, n);
+    if (n > kWarpEntries) {
+      if (lane == 0) {
+        sm.bound[warp] = bound;
+        atomicOr(&sm.heavy, 1 << warp);
       }
-      n = __reduce_add_sync(kFull, n);
-      heavy = n > kWarpEntries;
-      if (lane == 0) heavy_bound[warp] = bound;
-      if (!heavy)
-        join_head<T, D, BK, 1, 1>(P, sm.warp[warp], 0, b, h, len, sp.np, bound, part,
-                                  [&](int i) { return sp.key0(i); });
+    } else {
+      join_head<T, D, BK, 1, 1>(P, sm.warp[warp], 0, r.b, r.h, r.len, bound, r.parts);
     }
   }
-  __shared__ int heavy_warps;
-  if (tid == 0) heavy_warps = 0;
   __syncthreads();
-  if (heavy && lane == 0) atomicOr(&heavy_warps, 1 << warp);
-  __syncthreads();
-  const int todo = heavy_warps;
-  if (__popc(todo) >= kHeadWarps / 2) {  // as fast a warp each as one after the other
-    if (heavy) {
-      const int b = static_cast<int>((row0 + warp) / P.Hq);
-      const int h = static_cast<int>(row0 + warp - static_cast<int64_t>(b) * P.Hq);
-      const int len = clamped_len(P, b);
-      const SplitParts sp(P, b, h, len);
-      join_head<T, D, BK, 1, 1>(P, sm.warp[warp], 0, b, h, len, sp.np, heavy_bound[warp],
-                                [&](int i) { return sp.part(i); },
-                                [&](int i) { return sp.key0(i); });
+  const int todo = sm.heavy;
+  if (__popc(todo) >= kJoinWarps / 2) {
+    if (todo >> warp & 1) {
+      const HeadRef r = head(warp);
+      join_head<T, D, BK, 1, 1>(P, sm.warp[warp], 0, r.b, r.h, r.len, sm.bound[warp], r.parts);
     }
     return;
   }
   for (int left = todo; left; left &= left - 1) {
     const int w = __ffs(left) - 1;
-    const int b = static_cast<int>((row0 + w) / P.Hq);
-    const int h = static_cast<int>(row0 + w - static_cast<int64_t>(b) * P.Hq);
-    const int len = clamped_len(P, b);
-    const SplitParts sp(P, b, h, len);
-    join_head<T, D, BK, kHeadWarps, 1>(P, sm.block, 0, b, h, len, sp.np, heavy_bound[w],
-                                       [&](int i) { return sp.part(i); },
-                                       [&](int i) { return sp.key0(i); });
+    const HeadRef r = head(w);
+    join_head<T, D, BK, kJoinWarps, 1>(P, sm.block, 0, r.b, r.h, r.len, sm.bound[w], r.parts);
     __syncthreads();  // shared memory of this head
   }
 }
 
+template <typename T, int D, int BK>
+__global__ void __launch_bounds__(32 * kJoinWarps) decode_join_many_kernel(const DecodeProblem P) {
+  __shared__ ManySmem sm;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t rows = static_cast<int64_t>(P.B) * P.Hq;
+  const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kJoinWarps;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  auto head = [&](int w) {
+    HeadRef r;
+    r.b = static_cast<int>((row0 + w) / P.Hq);
+    r.h = static_cast<int>(row0 + w - static_cast<int64_t>(r.b) * P.Hq);
+    r.len = clamped_len(P, r.b);
+    r.parts = split_parts(P, r.b, r.h, r.len);
+    return r;
+  };
+  bool valid = row0 + warp < rows;
+  if (valid) {
+    const int b = static_cast<int>((row0 + warp) / P.Hq);
+    const int h = static_cast<int>(row0 + warp - static_cast<int64_t>(b) * P.Hq);
+    const int raw_len = P.lens[b];
+    if (clamped_len(P, b) == 0) {
+      write_empty<T, D>(P, b, h, raw_len == 0, lane, 32);
+      valid = false;
+    }
+  }
+  join_many<T, D, BK>(P, sm, valid, head);
+}
+
+// Allows a kernel more than 48 KB of shared memory, once per device.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 template <typename T, int D, int NT>
 cudaError_t launch_scores(const DecodeProblem& P, cudaStream_t s) {
-  const size_t smem = (sizeof(T) == 4 ? kScoreWarps * 8 * NT * D * sizeof(float) : 0) +
-                      sizeof(int) * (P.B + 1);
+  auto bytes = [](int B) {
+    return (sizeof(T) == 4 ? kScoreWarps * 8 * NT * D * sizeof(float) : 0) + sizeof(int) * (B + 1);
+  };
   auto kern = decode_scores_kernel<T, D, NT>;
-  if (smem > 47 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
-    if (e != cudaSuccess) return e;
-  }
+  static std::atomic<uint64_t> done{0};
+  const cudaError_t e = allow_smem(kern, bytes(kMaxRequests), done);
+  if (e != cudaSuccess) return e;
+  const size_t smem = bytes(P.B);
   kern<<<kDecodeScoreWarps / kScoreWarps, kScoreThreads, smem, s>>>(P);
   return cudaGetLastError();
 }
@@ -1084,8 +1118,8 @@ cudaError_t launch_join(const DecodeProblem& P, cudaStream_t s) {
   cfg.numAttrs = P.join_blocks > 1 ? 2 : 1;
   if (P.join_blocks == 0) {
     const int64_t rows = static_cast<int64_t>(P.B) * P.Hq;
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + kHeadWarps - 1) / kHeadWarps));
-    cfg.blockDim = dim3(32 * kHeadWarps);
+    cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+    cfg.blockDim = dim3(32 * kJoinWarps);
     return cudaLaunchKernelEx(&cfg, decode_join_many_kernel<T, D, BK>, P);
   }
   cfg.gridDim = dim3(P.join_blocks, P.Hq, P.B);
@@ -1098,35 +1132,39 @@ cudaError_t launch_join(const DecodeProblem& P, cudaStream_t s) {
 
 // ------------------------------------------------------------------ cluster: one kernel --
 
-constexpr int kClusterBlocks = 8;
-constexpr int kClusterWarps = 8;  // per block
-constexpr int kClusterParts = kClusterBlocks * kClusterWarps;
-
-// A cluster of 8 blocks scores one (request, head group), each of its 64 warps an equal run of
-// units, and after a cluster barrier its blocks join the group's heads.  One launch and no prefix
-// sums: less latency than the split kernels, which only the batch's longest requests repay.
+// A cluster of P.cluster (1 to 8) blocks scores one (request, head group), each of its warps an
+// equal run of units, and after a cluster barrier its blocks join the group's heads.  One launch
+// and no prefix sums: less latency than the split kernels, as long as all clusters run at once.
 template <typename T, int D, int NT, int BK>
-__global__ void __launch_bounds__(32 * kClusterWarps, 2)
-    decode_cluster_kernel(const DecodeProblem P) {
-  __shared__ JoinSmem<kClusterWarps> sm;
+__global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(const DecodeProblem P) {
+  __shared__ union {
+    JoinSmem<kJoinWarps> block;
+    ManySmem many;
+  } sm;
   __shared__ __align__(16) float sq[sizeof(T) == 4 ? 8 * NT * D : 4];
   __shared__ int known[8 * NT];  // ordered(): the largest score of each head in the cluster so far
   const int tid = threadIdx.x, warp = tid >> 5;
-  const int rank = blockIdx.x;  // the cluster is the x extent of the grid
+  const int blocks = P.cluster, rank = blockIdx.x;  // the cluster is the x extent of the grid
   const int hg = blockIdx.y, b = blockIdx.z;
   const int HG = P.Hkv * P.head_blocks;
   if (tid < 8 * NT) known[tid] = ordered(-INFINITY);
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const int raw_len = P.lens[b], len = clamped_len(P, b);
-  const int nb = (len + 15) >> 4, run = (nb + kClusterParts - 1) / kClusterParts;
-  int2* parts = P.parts + (static_cast<int64_t>(b) * HG + hg) * kClusterParts * (8 * NT);
+  Parts parts;
+  parts.np = blocks * kJoinWarps;
+  parts.nb = (len + 15) >> 4;
+  parts.run = (parts.nb + parts.np - 1) / parts.np;
+  parts.off = 0;
+  parts.stride = 8 * NT;
+  int2* info = P.parts + (static_cast<int64_t>(b) * HG + hg) * parts.np * (8 * NT);
   if (len > 0) {
     Scorer<T, D, NT> sc;
-    sc.load_q(P, b, hg, sq, tid, 32 * kClusterWarps);
+    sc.load_q(P, b, hg, sq, tid, 32 * kJoinWarps);
     if (sizeof(T) == 4) __syncthreads();
-    const int part = rank * kClusterWarps + warp;
-    score_run<T, D, NT, true>(P, sc, sq, b, hg, len, min(part * run, nb),
-                              min(part * run + run, nb), parts + part * (8 * NT), known);
+    const int i = rank * kJoinWarps + warp;
+    score_run<T, D, NT, true>(P, sc, sq, b, hg, len, min(i * parts.run, parts.nb),
+                              min((i + 1) * parts.run, parts.nb), info + i * (8 * NT), known,
+                              blocks);
   } else {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (raw_len != 0 && rank == 0 && hg == 0 && tid == 0)
@@ -1134,31 +1172,39 @@ __global__ void __launch_bounds__(32 * kClusterWarps, 2)
   }
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+  // the block's heads: rank, rank + blocks, ...
   const int hk = hg / P.head_blocks, hb = hg - hk * P.head_blocks;
   const int h0 = hk * P.G + hb * 8 * NT, heads = min(8 * NT, P.G - hb * 8 * NT);
-  for (int col = rank; col < heads; col += kClusterBlocks) {
-    if (len == 0) {
-      write_empty<T, D>(P, b, h0 + col, raw_len == 0, tid, 32 * kClusterWarps);
-      continue;
+  if (len == 0) {
+    for (int col = rank; col < heads; col += blocks)
+      write_empty<T, D>(P, b, h0 + col, raw_len == 0, tid, 32 * kJoinWarps);
+  } else if (heads <= blocks) {
+    if (rank >= heads) return;
+    parts.info = info + rank;
+    const Bounds bound = part_bounds<BK, kJoinWarps>(P, sm.block.red, parts);
+    join_head<T, D, BK, kJoinWarps, 1>(P, sm.block, 0, b, h0 + rank, len, bound, parts);
+  } else {
+    for (int c0 = rank; c0 < heads; c0 += blocks * kJoinWarps) {
+      auto head = [&](int w) {
+        HeadRef r{b, h0 + c0 + w * blocks, len, parts};
+        r.parts.info = info + c0 + w * blocks;
+        return r;
+      };
+      join_many<T, D, BK>(P, sm.many, c0 + warp * blocks < heads, head);
+      __syncthreads();
     }
-    __syncthreads();  // shared memory of the previous head
-    auto part = [&](int i) { return parts[i * (8 * NT) + col]; };
-    const Bounds bound = part_bounds<BK, kClusterWarps>(P, sm.red, kClusterParts, part);
-    join_head<T, D, BK, kClusterWarps, 1>(
-        P, sm, 0, b, h0 + col, len, kClusterParts, bound, part,
-        [&](int i) { return min(i * run, nb) * 16; });
   }
 }
 
 template <typename T, int D, int NT, int BK>
 cudaError_t launch_cluster(const DecodeProblem& P, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kClusterBlocks, P.Hkv * P.head_blocks, P.B);
-  cfg.blockDim = dim3(32 * kClusterWarps);
+  cfg.gridDim = dim3(P.cluster, P.Hkv * P.head_blocks, P.B);
+  cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = s;
   cudaLaunchAttribute attr = {};
   attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = kClusterBlocks;
+  attr.val.clusterDim.x = P.cluster;
   attr.val.clusterDim.y = 1;
   attr.val.clusterDim.z = 1;
   cfg.attrs = &attr;

@@ -110,12 +110,12 @@ struct DecodeProblem {
   int n_iter;
   float alpha, beta, c;
   int score_warps;
-  int cluster;    // one kernel of clusters instead of the split kernels
-  int join_blocks;  // blocks of 8 warps per head of the split kernels' join; 0 = one warp per head
+  int cluster;      // blocks per cluster of the one-launch kernel; 0 = the split kernels
+  int join_blocks;  // blocks of 8 warps per head of the split kernels' join (1 or 4); 0 = a warp
   // workspace
   int32_t* pre;         // [B + 1] prefix sums of the requests' 16-key units
   int2* parts;          // (count, max bits): [score_warps + groups][heads_per_block], or with
-                        // clusters [groups][64][heads_per_block]; groups = B Hkv head_blocks
+                        // clusters [groups][8 cluster][heads_per_block]; groups = B Hkv head_blocks
   int2* cand;           // [B][Hq][cand_stride] (z bits, key)
   int64_t cand_stride;  // max_len rounded up to 16
 };

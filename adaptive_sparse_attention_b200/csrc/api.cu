@@ -789,7 +789,11 @@ int entmax_attn_decode(const void* q, long long q_stride_b, long long q_stride_h
   P.beta = beta;
   P.c = static_cast<float>((a - 1.0) / std::sqrt(static_cast<double>(d)));
   choose_decode_kernels(&P, static_cast<double>(d * esz));
-  const cudaError_t e = ea::launch_decode(P, dtype, d, stream);
+  cudaError_t e;
+  if (dtype == ENTMAX_ATTN_FP32)
+    e = d == 64 ? ea::launch_decode_fp32_64(P, stream) : ea::launch_decode_fp32_128(P, stream);
+  else
+    e = d == 64 ? ea::launch_decode_bf16_64(P, stream) : ea::launch_decode_bf16_128(P, stream);
   return e == cudaSuccess ? ENTMAX_ATTN_OK : cuda_fail(e);
 }
 

@@ -1,4 +1,4 @@
-// decode.cu -- alpha-entmax attention of one new token per request over a paged key-value cache
+// decode.cuh -- alpha-entmax attention of one new token per request over a paged key-value cache
 // (the serving form of the forward pass).  For request b with n = seq_lens[b] keys and query head
 // h of kv head h / G:
 //   z_j = c q . k_j, c = (alpha - 1) / sqrt(d);   p_j = [z_j - tau]_+^beta, sum_j p_j = 1;
@@ -12,11 +12,13 @@
 // traffic is that of the keys alone unless the supports are wide.
 //
 // What bounds it: HBM reads of the keys.  The cache is split in units of 16 keys of one kv head;
-// all units of the batch are dealt to the grid's warps in contiguous runs of one length, whatever the
-// requests' lengths, so one long request and many ragged ones load the GPU alike, and the lengths
-// are needed on the device only.  A run that crosses from one (request, kv head) to the next is
+// all units of the batch are dealt to the grid's warps in contiguous runs of one length, whatever
+// the requests' lengths, so one long request and many ragged ones load the GPU alike, and the
+// lengths are needed on the device only.  A run that crosses from one (request, kv head) to the next is
 // cut there into parts; part (warp w, group g) has the number w + g, which is unique because
 // every cut advances w or g.
+#pragma once
+
 #include <cuda_bf16.h>
 
 #include <atomic>
@@ -31,7 +33,6 @@ namespace {
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
 constexpr int kNewtonSteps = 64;  // a bound that no search reaches
-constexpr int kFew = 128;   // candidates of a head that need no better bound than m - 1
 constexpr int kSolo = 256;  // candidates of a head that one warp takes alone
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -103,6 +104,15 @@ __device__ __forceinline__ float unordered(int i) {
   return __int_as_float(i ^ ((i >> 31) & 0x7fffffff));
 }
 
+// x = *p if go
+__device__ __forceinline__ void load_stream_if(uint4& x, const void* p, bool go) {
+  asm volatile(
+      "{ .reg .pred q; setp.ne.s32 q, %5, 0;\n\t"
+      "@q ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4]; }"
+      : "+r"(x.x), "+r"(x.y), "+r"(x.z), "+r"(x.w)
+      : "l"(p), "r"(static_cast<int>(go)));
+}
+
 // Scores of 16 keys x 8 NT heads.  Lane 4 g + t holds, of key rows g and g + 8, the 16-byte chunks
 // t, t + 4, t + 8, ... (four lanes read 64 contiguous bytes of a row).  bf16: the chunk's four
 // bf16 pairs are the A fragments of two m16n8k16 products whose k index is permuted the same way
@@ -143,12 +153,15 @@ struct Scorer<__nv_bfloat16, D, NT> {
                                          const float*) const {
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+      float other[4] = {};  // two chains of products: half the latency of one
       acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.f;
 #pragma unroll
       for (int c = 0; c < kChunks; ++c) {
         mma_bf16(acc[n], a[0][c].x, a[1][c].x, a[0][c].y, a[1][c].y, bq[n][c][0], bq[n][c][1]);
-        mma_bf16(acc[n], a[0][c].z, a[1][c].z, a[0][c].w, a[1][c].w, bq[n][c][2], bq[n][c][3]);
+        mma_bf16(other, a[0][c].z, a[1][c].z, a[0][c].w, a[1][c].w, bq[n][c][2], bq[n][c][3]);
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] += other[i];
     }
   }
 };
@@ -229,14 +242,15 @@ struct RowCursor {
 
 // One warp scores units [first, last) of 16 keys of head group hg of request b and appends the
 // candidates of each head to the group's lists at the run's first key, a count and a max per head
-// to part.  sq: the warp's (or block's) shared-memory q rows, fp32 only.  SHARE: the warps of a cluster of `blocks` blocks, all at the
-// same heads, tell each other the largest score that they have met (known, one copy per block), so
-// that each keeps few candidates beside those of the end: which ones depends on the timing, but the
-// join drops all of them again.
+// to part.  sq: the warp's (or block's) shared-memory q rows, fp32 only.  SHARE: the warps of a
+// cluster of `blocks` blocks, all at the same heads, tell each other the largest score that they
+// have met (known, one copy per block), so that each keeps few candidates beside those of the end:
+// which ones depends on the timing, but the join drops all of them again.
 template <typename T, int D, int NT, bool SHARE>
 __device__ __forceinline__ void score_run(const DecodeProblem& P,
-                                          const Scorer<T, D, NT>& sc, const float* sq, int b, int hg, int len, int first,
-                                          int last, int2* part, int* known, int blocks) {
+                                          const Scorer<T, D, NT>& sc, const float* sq, int b,
+                                          int hg, int len, int first, int last, int2* part,
+                                          int* known, int blocks) {
   using S = Scorer<T, D, NT>;
   constexpr int CH = S::kChunks;
   // 8 KB of keys in flight per warp, in registers: 128 KB per SM with 16 warps, which reads at 6.2
@@ -269,42 +283,43 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
   bool bad_page = false;
 
   // Pipeline: the keys of the next DEPTH units are in registers or on their way, the page numbers
-  // of the unit after those too.
+  // of the unit after those too.  No load is predicated per row: rows past the last key take the
+  // page of the last key, and a page that does not exist page 0 (the part is then marked NaN), so
+  // every address lies in the cache; their scores are masked below.
+  const int page_size = P.page_size, last_blk = (len - 1) / page_size;
   RowCursor cur[2];
-  cur[0].start(first * 16 + g, P.page_size);
-  cur[1].start(first * 16 + g + 8, P.page_size);
+  cur[0].start(first * 16 + g, page_size);
+  cur[1].start(first * 16 + g + 8, page_size);
   int fetch = first;  // unit the cursors stand at
   int page[2], off[2];
   auto next_pages = [&]() {
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      page[i] = -1;
       off[i] = cur[i].off;
-      if (fetch < last && fetch * 16 + g + 8 * i < len) {
-        page[i] = table[cur[i].blk];
-        if (page[i] < 0 || page[i] >= P.num_pages) {
-          page[i] = -1;
-          bad_page = true;
-        }
-      }
-      cur[i].advance(P.page_size);
+      page[i] = table[min(cur[i].blk, last_blk)];
+      cur[i].advance(page_size);
     }
-    ++fetch;
   };
   uint4 unit[DEPTH][2][CH];
   auto load_unit = [&](uint4 (&x)[2][CH]) {
+    const bool go = fetch < last;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      const T* row = kbase + page[i] * P.page_stride + off[i] * P.slot_stride;
+      const bool exists = static_cast<unsigned>(page[i]) < static_cast<unsigned>(P.num_pages);
+      bad_page |= !exists;
+      const T* row = kbase + (exists ? page[i] : 0) * P.page_stride + off[i] * P.slot_stride;
 #pragma unroll
-      for (int c = 0; c < CH; ++c)
-        x[i][c] = page[i] >= 0 ? load_stream(row + c * (64 / sizeof(T)))
-                               : make_uint4(0u, 0u, 0u, 0u);
+      for (int c = 0; c < CH; ++c) load_stream_if(x[i][c], row + c * (64 / sizeof(T)), go);
     }
+    ++fetch;
   };
   next_pages();
 #pragma unroll
   for (int i = 0; i < DEPTH; ++i) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int c = 0; c < CH; ++c) unit[i][r][c] = make_uint4(0u, 0u, 0u, 0u);
     load_unit(unit[i]);
     next_pages();
   }
@@ -320,42 +335,56 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
         load_unit(unit[i]);
         next_pages();
         const int key = blk * 16 + g;
-        bool above = false, pass = false;
+        bool pass = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float z0 = fmaf(P.c, acc[n][e], none[n][e]);
-            float z1 = fmaf(P.c, acc[n][2 + e], none[n][e]);
-            if (key >= len) z0 = -INFINITY;
-            if (key + 8 >= len) z1 = -INFINITY;
-            acc[n][e] = z0;
-            acc[n][2 + e] = z1;
-            own[n][e] = max_nan(own[n][e], max_nan(z0, z1));
-            if (SHARE)
-              m[n][e] = fmaxf(m[n][e],
-                              unordered(*static_cast<volatile int*>(known + n * 8 + 2 * t + e)));
-            const float top = fmaxf(z0, z1);
-            above |= top > m[n][e];
+            acc[n][e] = fmaf(P.c, acc[n][e], none[n][e]);
+            acc[n][2 + e] = fmaf(P.c, acc[n][2 + e], none[n][e]);
+          }
+        if (blk * 16 + 16 > len) {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key + 8 * (e >> 1) >= len) acc[n][e] = -INFINITY;
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float top = max_nan(acc[n][e], acc[n][2 + e]);
+            own[n][e] = max_nan(own[n][e], top);
             pass |= top > m[n][e] - 1.f;
           }
-        if (__any_sync(kFull, above)) {  // a new maximum
+        if (__any_sync(kFull, pass)) {
+          bool above = false;
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float x = fmaxf(acc[n][e], acc[n][2 + e]);
-#pragma unroll
-              for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
-              if (SHARE && x > m[n][e] && g < blocks)  // lane 4 g + t tells block g
-                asm volatile("red.relaxed.cluster.shared::cluster.max.s32 [%0], %1;" ::"r"(
-                                 remote(known + n * 8 + 2 * t + e, g)),
-                             "r"(ordered(x))
-                             : "memory");
-              m[n][e] = fmaxf(m[n][e], x);
+              if (SHARE)
+                m[n][e] = fmaxf(
+                    m[n][e], unordered(*static_cast<volatile int*>(known + n * 8 + 2 * t + e)));
+              above |= fmaxf(acc[n][e], acc[n][2 + e]) > m[n][e];
             }
-        }
-        if (__any_sync(kFull, pass)) {  // (with the maximum of before: a superset)
+          if (__any_sync(kFull, above)) {  // a new maximum
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                float x = fmaxf(acc[n][e], acc[n][2 + e]);
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) x = fmaxf(x, __shfl_xor_sync(kFull, x, o));
+                if (SHARE && x > m[n][e] && g < blocks)  // lane 4 g + t tells block g
+                  asm volatile("red.relaxed.cluster.shared::cluster.max.s32 [%0], %1;" ::"r"(
+                                   remote(known + n * 8 + 2 * t + e, g)),
+                               "r"(ordered(x))
+                               : "memory");
+                m[n][e] = fmaxf(m[n][e], x);
+              }
+          }
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -509,8 +538,9 @@ struct Parts {
 // are scores of the head, and the tau of a part of the keys is at most that of all (more keys only
 // add to the sum), so a few of the steps above on up to 256 of them give a bound far above m - 1:
 // of 20000 normal scores at alpha = 1.333, 184 lie above tau, 226 above the bound from 64 maxima
-// and 3496 above m - 1 (with few candidates it is m - 1: the steps cost more than they save).
-// Every warp computes both, so that they need no barrier; red: for more
+// and 3496 above m - 1.  Where at most half of the parts reach above m - 1 the candidates are few
+// and the bound is m - 1.  (The parts' counts do not enter: in the cluster kernel they depend on
+// the timing, and the bound decides in which order the sums below add.)  Every warp computes both, so that they need no barrier; red: for more
 // than 256 parts, whose maximum the block takes together.
 struct Bounds {
   float m, floor;
@@ -522,18 +552,11 @@ __device__ __forceinline__ Bounds part_bounds(const DecodeProblem& P, float* red
   constexpr int R = 8;
   const int lane = threadIdx.x & 31;
   float x[R];
-  int count[R];
   Bounds r;
   r.m = -INFINITY;
 #pragma unroll
   for (int j = 0; j < R; ++j) {
-    x[j] = -INFINITY;
-    count[j] = 0;
-    if (lane + 32 * j < np) {
-      const int2 y = parts.part(lane + 32 * j);
-      x[j] = __int_as_float(y.y);
-      count[j] = y.x;
-    }
+    x[j] = lane + 32 * j < np ? __int_as_float(parts.part(lane + 32 * j).y) : -INFINITY;
     r.m = max_nan(r.m, x[j]);
   }
   if (np > 32 * R)
@@ -549,12 +572,10 @@ __device__ __forceinline__ Bounds part_bounds(const DecodeProblem& P, float* red
     for (int o = W / 2; o > 0; o >>= 1) r.m = max_nan(r.m, __shfl_xor_sync(kFull, r.m, o));
   }
   r.floor = r.m - 1.f;
-  int n = 0;  // candidates above m - 1
+  int n = 0;  // parts that reach above m - 1
 #pragma unroll
-  for (int j = 0; j < R; ++j)
-    if (x[j] > r.floor) n += count[j];
-  n = __reduce_add_sync(kFull, n);
-  if (n > kFew && (BK != kBetaGeneral || P.beta >= 1.f)) {
+  for (int j = 0; j < R; ++j) n += __popc(__ballot_sync(kFull, x[j] > r.floor));
+  if (2 * n > min(np, 32 * R) && (BK != kBetaGeneral || P.beta >= 1.f)) {
     for (int it = 0; it < 3; ++it) {
       float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -989,8 +1010,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
   join_head<T, D, BK, kJoinWarps, C>(P, sm, rank, b, h, len, bound, parts);
 }
 
-// One warp per head, up to eight heads to a block; a head with more than kWarpEntries candidates
-// is left to the whole block, unless half of the warps have one.
+// One warp per head, up to eight heads to a block.  DEFER: a head with more than kWarpEntries
+// candidates is left to the whole block, unless half of the warps have one.  (Not in the cluster
+// kernel, where the counts depend on the timing; its requests are short.)
 constexpr int kWarpEntries = 768;
 struct ManySmem {
   union {
@@ -1005,22 +1027,24 @@ struct HeadRef {
   int b, h, len;
   Parts parts;
 };
-template <typename T, int D, int BK, typename Head>
+template <typename T, int D, int BK, bool DEFER, typename Head>
 __device__ __forceinline__ void join_many(const DecodeProblem& P, ManySmem& sm, bool valid,
                                           const Head& head) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  if (threadIdx.x == 0) sm.heavy = 0;
-  __syncthreads();
+  if (DEFER) {
+    if (threadIdx.x == 0) sm.heavy = 0;
+    __syncthreads();
+  }
   if (valid) {
     const HeadRef r = head(warp);
     const Bounds bound = part_bounds<BK, 1>(P, nullptr, r.parts);
     int n = 0;
-    for (int i = lane; i < r.parts.np; i += 32) {
-      const int2 x = r.parts.part(i);
-      if (__int_as_float(x.y) > bound.floor) n += x.x;
-    }
-    n = __reduce_add_sync(kFull, n);
-    if (n > kWarpEntries) {
+    if (DEFER)
+      for (int i = lane; i < r.parts.np; i += 32) {
+        const int2 x = r.parts.part(i);
+        if (__int_as_float(x.y) > bound.floor) n += x.x;
+      }
+    if (DEFER && __reduce_add_sync(kFull, n) > kWarpEntries) {
       if (lane == 0) {
         sm.bound[warp] = bound;
         atomicOr(&sm.heavy, 1 << warp);
@@ -1029,6 +1053,7 @@ __device__ __forceinline__ void join_many(const DecodeProblem& P, ManySmem& sm, 
       join_head<T, D, BK, 1, 1>(P, sm.warp[warp], 0, r.b, r.h, r.len, bound, r.parts);
     }
   }
+  if (!DEFER) return;
   __syncthreads();
   const int todo = sm.heavy;
   if (__popc(todo) >= kJoinWarps / 2) {
@@ -1071,7 +1096,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_many_kernel(const
       valid = false;
     }
   }
-  join_many<T, D, BK>(P, sm, valid, head);
+  join_many<T, D, BK, true>(P, sm, valid, head);
 }
 
 // Allows a kernel more than 48 KB of shared memory, once per device.
@@ -1190,8 +1215,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(cons
         r.parts.info = info + c0 + w * blocks;
         return r;
       };
-      join_many<T, D, BK>(P, sm.many, c0 + warp * blocks < heads, head);
-      __syncthreads();
+      join_many<T, D, BK, false>(P, sm.many, c0 + warp * blocks < heads, head);
     }
   }
 }
@@ -1234,12 +1258,4 @@ cudaError_t launch_decode_t(const DecodeProblem& P, cudaStream_t s) {
 }
 
 }  // namespace
-
-cudaError_t launch_decode(const DecodeProblem& P, int dtype, int d, cudaStream_t s) {
-  if (dtype == ENTMAX_ATTN_FP32)
-    return d == 64 ? launch_decode_t<float, 64>(P, s) : launch_decode_t<float, 128>(P, s);
-  return d == 64 ? launch_decode_t<__nv_bfloat16, 64>(P, s)
-                 : launch_decode_t<__nv_bfloat16, 128>(P, s);
-}
-
 }  // namespace ea

@@ -119,7 +119,10 @@ struct DecodeProblem {
   int2* cand;           // [B][Hq][cand_stride] (z bits, key)
   int64_t cand_stride;  // max_len rounded up to 16
 };
-cudaError_t launch_decode(const DecodeProblem& P, int dtype, int d, cudaStream_t s);
+cudaError_t launch_decode_bf16_64(const DecodeProblem& P, cudaStream_t s);
+cudaError_t launch_decode_bf16_128(const DecodeProblem& P, cudaStream_t s);
+cudaError_t launch_decode_fp32_64(const DecodeProblem& P, cudaStream_t s);
+cudaError_t launch_decode_fp32_128(const DecodeProblem& P, cudaStream_t s);
 
 // Records e as the string entmax_attn_last_cuda_error reports and returns ENTMAX_ATTN_ECUDA.
 int record_cuda_error(cudaError_t e);

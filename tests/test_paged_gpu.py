@@ -273,6 +273,22 @@ def test_decode_same_bits_again_and_dirty_workspace(oracle):
     assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("lens,Hq,Hkv,alpha,spikes", [
+    ([1000], 32, 8, 1.5, 0.02), ([4096] * 4, 8, 2, 1.333, 0.0), ([2000, 900, 1500], 16, 1, 2.0, 0.0),
+    ([700] * 40, 8, 4, 1.333, 0.0), ([3000] * 16, 8, 8, 1.5, 0.0), ([20000, 8000], 8, 2, 1.333, 0.0)])
+def test_decode_same_bits_many_times(lens, Hq, Hkv, alpha, spikes):
+    """The warps of a cluster share their running maxima, so which candidates they store depends on
+    the timing; the results must not."""
+    c = Case(lens, Hq, Hkv, 64, 16, "bf16", seed=15, spikes=spikes)
+    ws = ea.alloc_decode_workspace(c.q, c.kc, max(lens))
+    first = None
+    for _ in range(40):
+        got = ea.entmax_attn_decode(c.q, c.kc, c.vc, c.d_tables, c.d_lens, alpha,
+                                    max_len=max(lens), workspace=ws)
+        first = first or got
+        assert torch.equal(got[0], first[0]) and torch.equal(got[1], first[1])
+
+
 def test_decode_layout_variants_agree():
     """[B, Hq, 1, d], given outputs, a table that is a slice of a wider one."""
     c = Case([500, 20], 4, 2, 64, 16, "bf16", seed=9)

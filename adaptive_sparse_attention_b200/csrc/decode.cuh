@@ -913,9 +913,8 @@ __global__ void __launch_bounds__(kScoreThreads, 4) decode_scores_kernel(const D
   int* pre = reinterpret_cast<int*>(
       smem + (sizeof(T) == 4 ? kScoreWarps * 8 * NT * D * sizeof(float) : 0));  // [B + 1]
   __shared__ int scan_buf[kScoreWarps];
-  asm volatile("griddepcontrol.launch_dependents;");
-
   const int tid = threadIdx.x, warp = tid >> 5;
+  serial_start();
   {  // prefix sums of the requests' unit counts
     const int per = (P.B + kScoreThreads - 1) / kScoreThreads;
     const int b0 = min(tid * per, P.B), b1 = min(b0 + per, P.B);
@@ -996,8 +995,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_kernel(const Deco
   __shared__ JoinSmem<kJoinWarps, C> sm;
   const int rank = C > 1 ? blockIdx.x : 0;
   const int h = blockIdx.y, b = blockIdx.z;
+  serial_wait();
   const int raw_len = P.lens[b], len = clamped_len(P, b);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (len == 0) {
     if (rank == 0) write_empty<T, D>(P, b, h, raw_len == 0, threadIdx.x, 32 * kJoinWarps);
     return;
@@ -1077,7 +1076,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_many_kernel(const
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t rows = static_cast<int64_t>(P.B) * P.Hq;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * kJoinWarps;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  serial_wait();
   auto head = [&](int w) {
     HeadRef r;
     r.b = static_cast<int>((row0 + w) / P.Hq);
@@ -1123,36 +1122,22 @@ cudaError_t launch_scores(const DecodeProblem& P, cudaStream_t s) {
   const cudaError_t e = allow_smem(kern, bytes(kMaxRequests), done);
   if (e != cudaSuccess) return e;
   const size_t smem = bytes(P.B);
-  kern<<<kDecodeScoreWarps / kScoreWarps, kScoreThreads, smem, s>>>(P);
-  return cudaGetLastError();
+  return launch_serial(kern, dim3(kDecodeScoreWarps / kScoreWarps), dim3(kScoreThreads), smem, s,
+                       1, P);
 }
 
-// The join after the score kernel, launched while it runs (griddepcontrol.wait holds it back).
 template <typename T, int D, int BK>
 cudaError_t launch_join(const DecodeProblem& P, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.stream = s;
-  cudaLaunchAttribute attr[2] = {};
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = P.join_blocks;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = P.join_blocks > 1 ? 2 : 1;
+  const dim3 block(32 * kJoinWarps);
   if (P.join_blocks == 0) {
     const int64_t rows = static_cast<int64_t>(P.B) * P.Hq;
-    cfg.gridDim = dim3(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
-    cfg.blockDim = dim3(32 * kJoinWarps);
-    return cudaLaunchKernelEx(&cfg, decode_join_many_kernel<T, D, BK>, P);
+    const dim3 grid(static_cast<unsigned>((rows + kJoinWarps - 1) / kJoinWarps));
+    return launch_serial(decode_join_many_kernel<T, D, BK>, grid, block, 0, s, 1, P);
   }
-  cfg.gridDim = dim3(P.join_blocks, P.Hq, P.B);
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  switch (P.join_blocks) {
-    case 4: return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, BK, 4>, P);
-    default: return cudaLaunchKernelEx(&cfg, decode_join_kernel<T, D, BK, 1>, P);
-  }
+  const dim3 grid(P.join_blocks, P.Hq, P.B);
+  return P.join_blocks == 4
+             ? launch_serial(decode_join_kernel<T, D, BK, 4>, grid, block, 0, s, 4, P)
+             : launch_serial(decode_join_kernel<T, D, BK, 1>, grid, block, 0, s, 1, P);
 }
 
 // ------------------------------------------------------------------ cluster: one kernel --
@@ -1173,6 +1158,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(cons
   const int hg = blockIdx.y, b = blockIdx.z;
   const int HG = P.Hkv * P.head_blocks;
   if (tid < 8 * NT) known[tid] = ordered(-INFINITY);
+  serial_start();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const int raw_len = P.lens[b], len = clamped_len(P, b);
   Parts parts;
@@ -1222,18 +1208,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(cons
 
 template <typename T, int D, int NT, int BK>
 cudaError_t launch_cluster(const DecodeProblem& P, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(P.cluster, P.Hkv * P.head_blocks, P.B);
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = s;
-  cudaLaunchAttribute attr = {};
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = P.cluster;
-  attr.val.clusterDim.y = 1;
-  attr.val.clusterDim.z = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, decode_cluster_kernel<T, D, NT, BK>, P);
+  return launch_serial(decode_cluster_kernel<T, D, NT, BK>,
+                       dim3(P.cluster, P.Hkv * P.head_blocks, P.B), dim3(32 * kJoinWarps), 0, s,
+                       P.cluster, P);
 }
 
 template <typename T, int D, int BK>

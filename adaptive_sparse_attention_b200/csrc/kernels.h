@@ -55,7 +55,39 @@ cudaError_t launch_entmax_rows(const void* x, int64_t ldx, void* p, int64_t ldp,
                                int rows, int n, float alpha, int n_iter, int dtype,
                                cudaStream_t s);
 
-// Paged key-value cache (paged.cu, decode.cu).
+// Paged key-value cache (paged.cu, decode.cuh).  Its kernels are a few microseconds each and follow
+// one another in a decoding step, so they are launched with programmatic stream serialization: a
+// kernel's blocks may be set up while the kernel before it in the stream still runs.  Each waits
+// (griddepcontrol.wait) for that kernel's end, its writes visible, before its first access to
+// memory, and lets the next one be set up from its own start on.
+template <typename K, typename... A>
+cudaError_t launch_serial(K kern, dim3 grid, dim3 block, size_t smem, cudaStream_t s, int cluster,
+                          const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2] = {};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void serial_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void serial_start() {
+  asm volatile("griddepcontrol.launch_dependents;");
+  serial_wait();
+}
+#endif
 constexpr int kMaxRequests = 8192;  // prefix sums over the batch live in shared memory
 
 // Block tables and slot maps of a step (entmax_attn_page_tables).

@@ -88,6 +88,7 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
   __shared__ int2 buf[kTableWarps];
   __shared__ int served_pages;
   const int tid = threadIdx.x;
+  serial_start();
   const int start = *P.free_start;
   const int avail = start >= 0 && start <= P.n_free ? P.n_free - start : 0;
   if (tid == 0) served_pages = 0;
@@ -202,6 +203,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
   char* dst = static_cast<char*>(blockIdx.z ? P.v_cache : P.k_cache) + lane * 16 +
               h * P.head_stride;
   const int n0 = blockIdx.x * (kStep * kAppendRows) + threadIdx.x / VPR;
+  serial_start();
   int64_t slot[kAppendRows];
   uint4 x[kAppendRows];
 #pragma unroll
@@ -240,8 +242,7 @@ cudaError_t launch_page_tables(const PageTables& P, cudaStream_t s) {
         page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
     if (e != cudaSuccess) return e;
   }
-  page_tables_kernel<<<grid, kTableThreads, smem, s>>>(P);
-  return cudaGetLastError();
+  return launch_serial(page_tables_kernel, dim3(grid), dim3(kTableThreads), smem, s, 1, P);
 }
 
 cudaError_t launch_paged_append(const PagedAppend& P, int row_bytes, cudaStream_t s) {
@@ -249,12 +250,12 @@ cudaError_t launch_paged_append(const PagedAppend& P, int row_bytes, cudaStream_
   const int per_block = kAppendThreads / vpr * kAppendRows;
   const dim3 grid(static_cast<unsigned>((P.n_tokens - 1) / per_block + 1),
                   static_cast<unsigned>(P.Hkv), 2);
+  const dim3 block(kAppendThreads);
   switch (vpr) {
-    case 8: paged_append_kernel<8><<<grid, kAppendThreads, 0, s>>>(P); break;
-    case 16: paged_append_kernel<16><<<grid, kAppendThreads, 0, s>>>(P); break;
-    default: paged_append_kernel<32><<<grid, kAppendThreads, 0, s>>>(P);
+    case 8: return launch_serial(paged_append_kernel<8>, grid, block, 0, s, 1, P);
+    case 16: return launch_serial(paged_append_kernel<16>, grid, block, 0, s, 1, P);
+    default: return launch_serial(paged_append_kernel<32>, grid, block, 0, s, 1, P);
   }
-  return cudaGetLastError();
 }
 
 }  // namespace ea

@@ -73,11 +73,14 @@ __device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// 16 bytes that are read once.  (Not ld.global.nc: a block may be set up while the kernel before it
+// still writes the cache, so the cache is not read-only for all of this kernel's life.)
 __device__ __forceinline__ uint4 load_stream(const void* p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-               : "l"(p));
+               : "l"(p)
+               : "memory");
   return r;
 }
 
@@ -108,9 +111,10 @@ __device__ __forceinline__ float unordered(int i) {
 __device__ __forceinline__ void load_stream_if(uint4& x, const void* p, bool go) {
   asm volatile(
       "{ .reg .pred q; setp.ne.s32 q, %5, 0;\n\t"
-      "@q ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4]; }"
+      "@q ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4]; }"
       : "+r"(x.x), "+r"(x.y), "+r"(x.z), "+r"(x.w)
-      : "l"(p), "r"(static_cast<int>(go)));
+      : "l"(p), "r"(static_cast<int>(go))
+      : "memory");
 }
 
 // Scores of 16 keys x 8 NT heads.  Lane 4 g + t holds, of key rows g and g + 8, the 16-byte chunks

@@ -39,7 +39,9 @@ def _load():
 
 
 def _on(stream, dev):
-    """A context that makes `stream` (a torch stream or a raw handle) current."""
+    """A context that makes `stream` (a torch stream or a raw handle) of `dev` current."""
+    if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
     if not isinstance(stream, torch.cuda.Stream):
         stream = torch.cuda.ExternalStream(
             stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), dev)

@@ -231,6 +231,31 @@ def test_decode_long_and_ragged(alpha, lens, oracle):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("alpha", [1.05, 1.1])
+@pytest.mark.parametrize("lens,Hq,Hkv", [([3000, 7, 1200], 4, 2), ([9000] * 2, 4, 1),
+                                         ([2500] * 12, 32, 16)])
+def test_decode_supports_as_wide_as_the_cache(dtype, alpha, lens, Hq, Hkv, oracle):
+    """alpha near 1: every key lies within 1 of the largest score (in z units) and most have p > 0,
+    so the candidates overflow the shared-memory lists; the cases take the cluster kernel and both
+    block joins of the split kernels."""
+    c = Case(lens, Hq, Hkv, 64, 16, dtype, seed=16, spikes=0.0)
+    out, tau = c.run(alpha)
+    c.check(out, tau, alpha, rows=range(min(3, len(lens))))
+
+
+@pytest.mark.parametrize("alpha,spikes", [(1.333, 0.0), (1.5, 0.02), (2.0, 0.0), (1.1, 0.0)])
+def test_decode_more_heads_than_blocks(alpha, spikes, oracle):
+    """Above 1024 heads the join takes a warp per head; some with more candidates than a warp is
+    given (those of the long requests), some with none."""
+    lens = ([5, 3000, 60, 0, 200, 1, 90, 1500, 17, 16] * 4)
+    c = Case(lens, 32, 8, 64, 16, "bf16", seed=17, spikes=spikes)
+    out, tau = c.run(alpha)
+    c.check(out, tau, alpha, rows=[0, 1, 3, 7, 12, 29, 39])
+    again = c.run(alpha)
+    assert torch.equal(out, again[0]) and torch.equal(tau, again[1])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
 @pytest.mark.parametrize("alpha,n_iter", [(1.333, 10), (1.5, 10), (2.0, 10), (3.0, 40)])
 def test_decode_equal_scores(dtype, alpha, n_iter, oracle):
     """q = 0: every key ties, p = 1/n, tau = -n^(1 - alpha); supports as wide as the cache."""

@@ -254,7 +254,7 @@ template <typename T, int D, int NT, bool SHARE>
 __device__ __forceinline__ void score_run(const DecodeProblem& P,
                                           const Scorer<T, D, NT>& sc, const float* sq, int b,
                                           int hg, int len, int first, int last, int2* part,
-                                          int* known, int blocks) {
+                                          int64_t part_stride, int* known, int blocks) {
   using S = Scorer<T, D, NT>;
   constexpr int CH = S::kChunks;
   // 8 KB of keys in flight per warp, in registers: 128 KB per SM with 16 warps, which reads at 6.2
@@ -417,7 +417,7 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) x = max_nan(x, __shfl_xor_sync(kFull, x, o));
       if (g == 0)  // NaN also stands for +inf and for a page that does not exist
-        part[n * 8 + 2 * t + e] =
+        part[(n * 8 + 2 * t + e) * part_stride] =
             make_int2(cnt[n][e], __float_as_int(x < INFINITY && !bad_page ? x : NAN));
     }
 }
@@ -529,12 +529,10 @@ __device__ __forceinline__ void warp_sum2(float& a, float& b) {
 
 // The parts of one (request, query head): part i holds the candidates of the keys from key0(i) on.
 struct Parts {
-  const int2* info;  // (count, max bits) of part 0
-  int stride, np;    // of info; number of parts
-  int run, off, nb;  // part i starts at unit i run - off of the nb units of the request
-  __device__ __forceinline__ int2 part(int i) const {
-    return info[static_cast<int64_t>(i) * stride];
-  }
+  const int2* info;      // (count, max bits) of each
+  int np;                // number of parts
+  int run, off, nb;      // part i starts at unit i run - off of the nb units of the request
+  __device__ __forceinline__ int2 part(int i) const { return info[i]; }
   __device__ __forceinline__ int key0(int i) const { return min(max(i * run - off, 0), nb) * 16; }
 };
 
@@ -910,6 +908,12 @@ __device__ __forceinline__ void write_empty(const DecodeProblem& P, int b, int h
 
 // ------------------------------------------------------------------ split: two kernels --
 
+// The split kernels keep the parts of one head of the groups (the first, second, ... of each
+// group) side by side: this many.
+__device__ __forceinline__ int64_t split_part_stride(const DecodeProblem& P) {
+  return P.score_warps + static_cast<int64_t>(P.B) * P.Hkv * P.head_blocks;
+}
+
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kScoreThreads, 4) decode_scores_kernel(const DecodeProblem P) {
   extern __shared__ __align__(16) char smem[];
@@ -969,8 +973,8 @@ __global__ void __launch_bounds__(kScoreThreads, 4) decode_scores_kernel(const D
     __syncwarp();
     score_run<T, D, NT, false>(
         P, sc, sq, b, hg, clamped_len(P, b), first, last,
-        P.parts + (static_cast<int64_t>(w) + static_cast<int64_t>(b) * HG + hg) * (8 * NT),
-        nullptr, 1);
+        P.parts + (static_cast<int64_t>(w) + static_cast<int64_t>(b) * HG + hg),
+        split_part_stride(P), nullptr, 1);
   }
 }
 
@@ -986,9 +990,7 @@ __device__ __forceinline__ Parts split_parts(const DecodeProblem& P, int b, int 
   const int w0 = A / r.run;
   r.off = A - w0 * r.run;
   r.np = (A + r.nb - 1) / r.run - w0 + 1;
-  r.stride = P.heads_per_block;
-  r.info = P.parts + (static_cast<int64_t>(w0) + static_cast<int64_t>(b) * HG + hg) * r.stride +
-           col;
+  r.info = P.parts + col * split_part_stride(P) + w0 + static_cast<int64_t>(b) * HG + hg;
   return r;
 }
 
@@ -1170,7 +1172,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(cons
   parts.nb = (len + 15) >> 4;
   parts.run = (parts.nb + parts.np - 1) / parts.np;
   parts.off = 0;
-  parts.stride = 8 * NT;
   int2* info = P.parts + (static_cast<int64_t>(b) * HG + hg) * parts.np * (8 * NT);
   if (len > 0) {
     Scorer<T, D, NT> sc;
@@ -1178,7 +1179,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(cons
     if (sizeof(T) == 4) __syncthreads();
     const int i = rank * kJoinWarps + warp;
     score_run<T, D, NT, true>(P, sc, sq, b, hg, len, min(i * parts.run, parts.nb),
-                              min((i + 1) * parts.run, parts.nb), info + i * (8 * NT), known,
+                              min((i + 1) * parts.run, parts.nb), info + i, parts.np, known,
                               blocks);
   } else {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -1195,14 +1196,14 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(cons
       write_empty<T, D>(P, b, h0 + col, raw_len == 0, tid, 32 * kJoinWarps);
   } else if (heads <= blocks) {
     if (rank >= heads) return;
-    parts.info = info + rank;
+    parts.info = info + rank * parts.np;
     const Bounds bound = part_bounds<BK, kJoinWarps>(P, sm.block.red, parts);
     join_head<T, D, BK, kJoinWarps, 1>(P, sm.block, 0, b, h0 + rank, len, bound, parts);
   } else {
     for (int c0 = rank; c0 < heads; c0 += blocks * kJoinWarps) {
       auto head = [&](int w) {
         HeadRef r{b, h0 + c0 + w * blocks, len, parts};
-        r.parts.info = info + c0 + w * blocks;
+        r.parts.info = info + (c0 + w * blocks) * parts.np;
         return r;
       };
       join_many<T, D, BK, false>(P, sm.many, c0 + warp * blocks < heads, head);

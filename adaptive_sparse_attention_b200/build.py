@@ -100,7 +100,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         for d in inc:
             cmd += ["-isystem" if d != INCLUDE else "-I", d]
         cmd += [src, "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
-                "-ltorch", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:" + os.path.basename(LIB),
+                "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:" + os.path.basename(LIB),
                 "-Wl,-rpath,$ORIGIN"]
         r = subprocess.run(cmd, capture_output=True, text=True)
         if verbose or r.returncode != 0:

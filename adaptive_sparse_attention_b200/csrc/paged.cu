@@ -88,7 +88,7 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
   __shared__ int2 buf[kTableWarps];
   __shared__ int served_pages;
   const int tid = threadIdx.x;
-  serial_start();
+  serial_wait();
   const int start = *P.free_start;
   const int avail = start >= 0 && start <= P.n_free ? P.n_free - start : 0;
   if (tid == 0) served_pages = 0;

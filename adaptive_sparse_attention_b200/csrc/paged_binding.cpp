@@ -8,6 +8,7 @@
 
 #include <ATen/ATen.h>
 #include <ATen/core/LegacyTypeDispatch.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -59,10 +60,23 @@ const at::Tensor& ints(PyObject* o, const char* name, int dim, at::Device dev) {
   return t;
 }
 
+at::Tensor empty(at::IntArrayRef shape, at::ScalarType type, at::Device dev) {
+  return at::detail::empty_cuda(shape, type, dev, c10::nullopt);
+}
+
+// Elements [from, from + n) of a 1-D tensor, as a tensor of its own on the same storage.
+at::Tensor piece(const at::Tensor& base, int64_t from, int64_t n) {
+  at::Tensor t = at::detail::make_tensor<c10::TensorImpl>(c10::Storage(base.storage()),
+                                                          base.key_set(), base.dtype());
+  t.unsafeGetTensorImpl()->set_storage_offset(from);
+  t.unsafeGetTensorImpl()->set_sizes_contiguous({n});
+  return t;
+}
+
 // The given output, or a new one; what was given has to be contiguous, of this shape and type.
 at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType type,
                   at::Device dev) {
-  if (o == Py_None) return at::empty(shape, at::TensorOptions(type).device(dev));
+  if (o == Py_None) return empty(shape, type, dev);
   const at::Tensor& t = tensor(o, name);
   if (t.sizes() != shape || t.scalar_type() != type || t.device() != dev || !t.is_contiguous())
     refuse("%s must be contiguous, of the documented shape and dtype, on the device of the inputs",
@@ -143,9 +157,19 @@ PyObject* page_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const c10::cuda::CUDAGuard on(dev);
     const at::Tensor slots = padded ? output(a[8], "slots", {B, n_new}, at::kLong, dev)
                                     : output(a[8], "slots", {n_new}, at::kLong, dev);
-    const at::Tensor lens_out = output(a[9], "lens_out", {B}, at::kInt, dev);
-    const at::Tensor cu = output(a[10], "cu_new", {B + 1}, at::kInt, dev);
-    const at::Tensor next = output(a[11], "free_next", {1}, at::kInt, dev);
+    at::Tensor lens_out, cu, next;
+    if (a[9] == Py_None && a[10] == Py_None && a[11] == Py_None) {
+      // one allocation, each 16-byte aligned (the packed forward pass wants cu_new so)
+      const int64_t at_lens = (B + 4) / 4 * 4, at_next = at_lens + (B + 3) / 4 * 4;
+      const at::Tensor all = empty({at_next + 1}, at::kInt, dev);
+      cu = piece(all, 0, B + 1);
+      lens_out = piece(all, at_lens, B);
+      next = piece(all, at_next, 1);
+    } else {
+      lens_out = output(a[9], "lens_out", {B}, at::kInt, dev);
+      cu = output(a[10], "cu_new", {B + 1}, at::kInt, dev);
+      next = output(a[11], "free_next", {1}, at::kInt, dev);
+    }
     const int rc = entmax_attn_page_tables(
         static_cast<const int32_t*>(lens.const_data_ptr()),
         static_cast<const int32_t*>(add.const_data_ptr()),
@@ -228,7 +252,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
       const size_t need = entmax_attn_decode_workspace_bytes(
           static_cast<int>(B), static_cast<int>(Hq), c.heads, max_len);
       if (need == 0) return PyLong_FromLong(ENTMAX_ATTN_EINVAL);
-      own = at::empty({static_cast<int64_t>(need)}, at::TensorOptions(at::kByte).device(c.dev));
+      own = empty({static_cast<int64_t>(need)}, at::kByte, c.dev);
     }
     const at::Tensor& ws = a[10] == Py_None ? own : tensor(a[10], "workspace");
     if (ws.device() != c.dev || !ws.is_contiguous())

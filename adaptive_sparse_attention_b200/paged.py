@@ -61,7 +61,7 @@ def page_tables(lens, new_lens, free_pages, free_start, block_tables, page_size:
     int32 [B + 1], the prefix sums of new_lens (the cu_seqlens of the packed forward pass); free_next
     int32 [1].  A request that does not fit keeps its length and gets slots of -1 (see
     include/entmax_attn.h).  The outputs may be given; lens_out and free_next may not be the
-    inputs themselves."""
+    inputs themselves.  Where none of lens_out, cu_new and free_next is, they share one storage."""
     if stream is not None:
         with _on(stream, lens.device):
             return page_tables(lens, new_lens, free_pages, free_start, block_tables, page_size,

@@ -1164,7 +1164,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(cons
   const int hg = blockIdx.y, b = blockIdx.z;
   const int HG = P.Hkv * P.head_blocks;
   if (tid < 8 * NT) known[tid] = ordered(-INFINITY);
-  serial_start();
+  serial_wait();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const int raw_len = P.lens[b], len = clamped_len(P, b);
   Parts parts;

@@ -922,7 +922,7 @@ __global__ void __launch_bounds__(kScoreThreads, 4) decode_scores_kernel(const D
       smem + (sizeof(T) == 4 ? kScoreWarps * 8 * NT * D * sizeof(float) : 0));  // [B + 1]
   __shared__ int scan_buf[kScoreWarps];
   const int tid = threadIdx.x, warp = tid >> 5;
-  serial_start();
+  serial_wait();
   {  // prefix sums of the requests' unit counts
     const int per = (P.B + kScoreThreads - 1) / kScoreThreads;
     const int b0 = min(tid * per, P.B), b1 = min(b0 + per, P.B);

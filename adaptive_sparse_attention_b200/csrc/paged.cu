@@ -203,7 +203,7 @@ __global__ void __launch_bounds__(kAppendThreads) paged_append_kernel(const Page
   char* dst = static_cast<char*>(blockIdx.z ? P.v_cache : P.k_cache) + lane * 16 +
               h * P.head_stride;
   const int n0 = blockIdx.x * (kStep * kAppendRows) + threadIdx.x / VPR;
-  serial_start();
+  serial_wait();
   int64_t slot[kAppendRows];
   uint4 x[kAppendRows];
 #pragma unroll

@@ -269,8 +269,9 @@ int entmax_attn_route_chunks(const void* q, const void* summaries, float* pi, fl
  * block_tables[b][j / page_size].  A token's "slot" is page * page_size + (slot in the page).
  * Any page_size >= 1; B at most 8192.
  *
- * The kernels are launched with programmatic stream serialization: their blocks may be set up while
- * the kernel before them in the stream still runs, and wait for its end before they touch memory.
+ * The kernels are launched with programmatic stream serialization: their blocks may be set up before
+ * the kernel before them in the stream has quite ended, and wait for its end before they touch
+ * memory.
  * The calls can be captured into graphs; make the first call of each on a device outside a capture
  * (it loads the kernels and looks up the status word).
  *

@@ -510,8 +510,7 @@ size_t decode_layout(void* base, int B, int Hq, int Hkv, int max_len, ea::Decode
   P->pre = reinterpret_cast<int32_t*>(p + off);
   off += align256(sizeof(int32_t) * (static_cast<size_t>(B) + 1));
   P->parts = reinterpret_cast<int2*>(p + off);
-  off += align256(sizeof(int2) *
-                  static_cast<size_t>(std::max(groups * 64, P->score_warps + groups)) *
+  off += align256(sizeof(int2) * static_cast<size_t>(P->score_warps + groups) *
                   P->heads_per_block);
   P->cand = reinterpret_cast<int2*>(p + off);
   off += align256(sizeof(int2) * static_cast<size_t>(B) * Hq * P->cand_stride);

@@ -91,6 +91,21 @@ __device__ __forceinline__ uint32_t remote(const void* p, int rank) {
   return r;
 }
 
+// Stores to the shared memory of another block.
+__device__ __forceinline__ void store_remote(uint32_t a, float x) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
+}
+__device__ __forceinline__ void store_remote(uint32_t a, int x) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
+}
+__device__ __forceinline__ void store_remote(uint32_t a, int2 x) {
+  asm volatile("st.shared::cluster.v2.s32 [%0], {%1, %2};" ::"r"(a), "r"(x.x), "r"(x.y)
+               : "memory");
+}
+__device__ __forceinline__ void store_remote(uint32_t a, float2 x) {
+  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x.x), "f"(x.y)
+               : "memory");
+}
 // max that keeps a NaN of either side
 __device__ __forceinline__ float max_nan(float a, float b) {
   float r;
@@ -246,7 +261,7 @@ struct RowCursor {
 
 // One warp scores units [first, last) of 16 keys of head group hg of request b and appends the
 // candidates of each head to the group's lists at the run's first key, a count and a max per head
-// to part.  sq: the warp's (or block's) shared-memory q rows, fp32 only.  SHARE: the warps of a
+// to part (SHARE: shared memory, of every block of the cluster).  sq: the warp's (or block's) shared-memory q rows, fp32 only.  SHARE: the warps of a
 // cluster of `blocks` blocks, all at the same heads, tell each other the largest score that they
 // have met (known, one copy per block), so that each keeps few candidates beside those of the end:
 // which ones depends on the timing, but the join drops all of them again.
@@ -416,9 +431,14 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
       float x = own[n][e];
 #pragma unroll
       for (int o = 4; o < 32; o <<= 1) x = max_nan(x, __shfl_xor_sync(kFull, x, o));
-      if (g == 0)  // NaN also stands for +inf and for a page that does not exist
-        part[(n * 8 + 2 * t + e) * part_stride] =
-            make_int2(cnt[n][e], __float_as_int(x < INFINITY && !bad_page ? x : NAN));
+      // NaN also stands for +inf and for a page that does not exist
+      const int2 y = make_int2(cnt[n][e], __float_as_int(x < INFINITY && !bad_page ? x : NAN));
+      int2* to = part + (n * 8 + 2 * t + e) * part_stride;
+      if (SHARE) {  // lane 4 g + t tells block g
+        if (g < blocks) store_remote(remote(to, g), y);
+      } else if (g == 0) {
+        *to = y;
+      }
     }
 }
 
@@ -470,17 +490,6 @@ __device__ __forceinline__ void join_sync() {
   }
 }
 
-// Stores to the shared memory of another block.
-__device__ __forceinline__ void store_remote(uint32_t a, float x) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(a), "f"(x) : "memory");
-}
-__device__ __forceinline__ void store_remote(uint32_t a, int x) {
-  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(a), "r"(x) : "memory");
-}
-__device__ __forceinline__ void store_remote(uint32_t a, float2 x) {
-  asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x.x), "f"(x.y)
-               : "memory");
-}
 // x into *p of every block of the join, by one warp
 template <int C, typename V>
 __device__ __forceinline__ void share(V* p, V x) {
@@ -728,6 +737,17 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
   float tau = 0.f;
   if (deal && warp != 0) {
     // waits for the first warp below
+  } else if (solo && n_list <= 32 && (BK != kBetaGeneral || P.beta >= 1.f)) {
+    const float z = lane < n_list ? entry(lane).x : -INFINITY;  // one each: no loop
+    tau = floor;
+    for (int it = 0; it < kNewtonSteps; ++it) {
+      float s0 = 0.f, s1 = 0.f;
+      norm_add<BK>(fmaxf(z - tau, 0.f), P.beta, s0, s1);
+      warp_sum2(s0, s1);
+      const float step = norm_step<BK>(s0, s1, P.beta);
+      tau += step;
+      if (!(step > 2.f * FLT_EPSILON * fmaxf(fabsf(tau), m - tau))) break;
+    }
   } else if (BK != kBetaGeneral || P.beta >= 1.f) {
     tau = floor;
     for (int it = 0; it < kNewtonSteps; ++it) {
@@ -1151,6 +1171,7 @@ cudaError_t launch_join(const DecodeProblem& P, cudaStream_t s) {
 // A cluster of P.cluster (1 to 8) blocks scores one (request, head group), each of its warps an
 // equal run of units, and after a cluster barrier its blocks join the group's heads.  One launch
 // and no prefix sums: less latency than the split kernels, as long as all clusters run at once.
+constexpr int kClusterBlocks = 8;  // at most
 template <typename T, int D, int NT, int BK>
 __global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(const DecodeProblem P) {
   __shared__ union {
@@ -1159,10 +1180,10 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(cons
   } sm;
   __shared__ __align__(16) float sq[sizeof(T) == 4 ? 8 * NT * D : 4];
   __shared__ int known[8 * NT];  // ordered(): the largest score of each head in the cluster so far
+  __shared__ int2 info[8 * NT * kClusterBlocks * kJoinWarps];  // [head][part]
   const int tid = threadIdx.x, warp = tid >> 5;
   const int blocks = P.cluster, rank = blockIdx.x;  // the cluster is the x extent of the grid
   const int hg = blockIdx.y, b = blockIdx.z;
-  const int HG = P.Hkv * P.head_blocks;
   if (tid < 8 * NT) known[tid] = ordered(-INFINITY);
   serial_wait();
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -1172,7 +1193,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(cons
   parts.nb = (len + 15) >> 4;
   parts.run = (parts.nb + parts.np - 1) / parts.np;
   parts.off = 0;
-  int2* info = P.parts + (static_cast<int64_t>(b) * HG + hg) * parts.np * (8 * NT);
   if (len > 0) {
     Scorer<T, D, NT> sc;
     sc.load_q(P, b, hg, sq, tid, 32 * kJoinWarps);

@@ -145,8 +145,8 @@ struct DecodeProblem {
   int join_blocks;  // blocks of 8 warps per head of the split kernels' join (1 or 4); 0 = a warp
   // workspace
   int32_t* pre;         // [B + 1] prefix sums of the requests' 16-key units
-  int2* parts;          // (count, max bits): [heads_per_block][score_warps + groups], or with
-                        // clusters [groups][heads_per_block][8 cluster]; groups = B Hkv head_blocks
+  int2* parts;          // (count, max bits) [heads_per_block][score_warps + groups], groups = B Hkv
+                        // head_blocks; the cluster kernel keeps its own in shared memory
   int2* cand;           // [B][Hq][cand_stride] (z bits, key)
   int64_t cand_stride;  // max_len rounded up to 16
 };

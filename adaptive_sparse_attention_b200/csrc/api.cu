@@ -523,14 +523,14 @@ size_t decode_layout(void* base, int B, int Hq, int Hkv, int max_len, ea::Decode
 //   cluster: C = 8, 4, 2 or 1 blocks per (request, head group), the most that run all at once (2
 //     blocks per SM).  One launch, about 5 us ahead of the split kernels (B = 1, 1000 keys: 10.4
 //     against 14.5; B = 16, 128 keys: 12.5 against 16.7; 4096 keys: 31 against 37), but a block
-//     reads about 44 GB/s, so a request much longer than the others, or alone, is late: 1 request of
-//     131072 keys takes 105 against 56.  So they serve a single request as long as its blocks' extra
-//     time against the 6.3 TB/s of the split kernels is below those 5 us, and a batch if its longest
-//     possible request is read in 12 us.
-//   join_blocks of the split kernels: up to 148 heads have a cluster of 4 blocks each (B = 4, lengths
-//     to 20000, alpha = 1.333 without spikes: 42 against 45 with one block), up to 1024 a block each
-//     (B = 16, 128 keys: 16.7 against 18.6 with a warp each), more a warp each (B = 64, 128 keys:
-//     20.7 against 31.2 with a block each).
+//     reads about 44 GB/s, so a request much longer than the others, or alone, is late: 1 request
+//     of 131072 keys takes 105 against 56.  So they serve a single request as long as its blocks'
+//     extra time against the 6.3 TB/s of the split kernels is below those 5 us, and a batch if its
+//     longest possible request is read in 12 us.
+//   join_blocks of the split kernels: up to 148 heads have a cluster of 4 blocks each (B = 4,
+//     lengths to 20000, alpha = 1.333 without spikes: 42 against 45 with one block), up to 1024 a
+//     block each (B = 16, 128 keys: 16.7 against 18.6 with a warp each), more a warp each (B = 64,
+//     128 keys: 20.7 against 31.2 with a block each).
 void choose_decode_kernels(ea::DecodeProblem* P, double row_bytes) {
   const int64_t groups = static_cast<int64_t>(P->B) * P->Hkv * P->head_blocks;
   P->cluster = 0;

@@ -80,8 +80,8 @@ __device__ __forceinline__ int last_at_most(const Entry* e, int n, int v) {
 
 // Every block scans the B lengths itself (a few KB from L2, no second launch and no order between
 // blocks), then writes its share of the new table entries and of the slots.  Bound by the launch
-// and three dependent loads for small batches (64 requests of one token: 5 us), by the search and
-// the writes of 8 bytes a token for large ones.
+// and three dependent loads for small batches (64 requests of one token: 5 us), by the scan, the
+// search and the writes of 8 bytes a token for large ones (1000 requests, 236K tokens: 6.8 us).
 __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTables P) {
   extern __shared__ __align__(16) char smem[];
   Entry* req = reinterpret_cast<Entry*>(smem);  // [B + 1], the last holds the totals
@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
 }
 
 // The copies of one chunk of tokens: a block takes kTokens tokens of one kv head of k or v, VPR
-// threads per row of VPR 16-byte vectors, U rows in flight per thread.  A pure copy: bound by HBM.
+// threads per row of VPR 16-byte vectors, kAppendRows rows in flight per thread.  A pure copy:
+// bound by HBM (32192 tokens of 8 heads, d = 128: 41 us, 6.4 TB/s; with one row in flight 57 us).
 // The rows of consecutive tokens are consecutive in a [Hkv, N, d] input and, within a page, in a
 // [pages, Hkv, page_size, d] cache.  The grid is (chunks of tokens, kv heads, k or v), so that no
 // index needs a 64-bit division.

@@ -24,6 +24,7 @@
 #include <cuda_bf16.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "common.cuh"
 #include "entmax_attn.h"
@@ -246,6 +247,13 @@ struct RowCursor {
     blk = key / page;
     off = key - blk * page;
   }
+  __device__ __forceinline__ void advance_in_pages_of_16(int page) {
+    off += 16;
+    if (off >= page) {
+      off -= page;
+      ++blk;
+    }
+  }
   __device__ __forceinline__ void advance(int page) {
     off += 16;
     if (off >= page) {
@@ -268,7 +276,9 @@ struct RowCursor {
 // same heads, tell each other the largest score that they have met (known, one copy per block), so
 // that each keeps few candidates beside those of the end: which ones depends on the timing, but the
 // join drops all of them again.
-template <typename T, int D, int NT, bool SHARE>
+// ONE_PAGE: page_size is a multiple of 16, so a unit lies in one page: one lookup for both rows of a
+// lane (33 requests with d = 64: 28.3 against 26.9 us; 64 of 16384 tokens 263 against 259).
+template <typename T, int D, int NT, bool SHARE, bool ONE_PAGE>
 __device__ __forceinline__ void score_run(const DecodeProblem& P,
                                           const Scorer<T, D, NT>& sc, const float* sq, int b,
                                           int hg, int len, int first, int last, int2* part,
@@ -315,11 +325,17 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
   int fetch = first;  // unit the cursors stand at
   int page[2], off[2];
   auto next_pages = [&]() {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      off[i] = cur[i].off;
-      page[i] = table[min(cur[i].blk, last_blk)];
-      cur[i].advance(page_size);
+    off[0] = cur[0].off;
+    page[0] = table[min(cur[0].blk, last_blk)];
+    if (ONE_PAGE) {
+      off[1] = off[0] + 8;
+      page[1] = page[0];
+      cur[0].advance_in_pages_of_16(page_size);
+    } else {
+      off[1] = cur[1].off;
+      page[1] = table[min(cur[1].blk, last_blk)];
+      cur[0].advance(page_size);
+      cur[1].advance(page_size);
     }
   };
   uint4 unit[DEPTH][2][CH];
@@ -1002,10 +1018,14 @@ __global__ void __launch_bounds__(kScoreThreads, 4) decode_scores_kernel(const D
     __syncwarp();
     sc.load_q(P, b, hg, sq, tid & 31, 32);
     __syncwarp();
-    score_run<T, D, NT, false>(
-        P, sc, sq, b, hg, clamped_len(P, b), first, last,
-        P.parts + (static_cast<int64_t>(w) + static_cast<int64_t>(b) * HG + hg),
-        split_part_stride(P), nullptr, 1);
+    auto score = [&](auto one_page) {
+      score_run<T, D, NT, false, decltype(one_page)::value>(
+          P, sc, sq, b, hg, clamped_len(P, b), first, last,
+          P.parts + (static_cast<int64_t>(w) + static_cast<int64_t>(b) * HG + hg),
+          split_part_stride(P), nullptr, 1);
+    };
+    if (P.page_size % 16 == 0) score(std::true_type());
+    else score(std::false_type());
   }
 }
 
@@ -1215,9 +1235,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(cons
     sc.load_q(P, b, hg, sq, tid, 32 * kJoinWarps);
     if (sizeof(T) == 4) __syncthreads();
     const int i = rank * kJoinWarps + warp;
-    score_run<T, D, NT, true>(P, sc, sq, b, hg, len, min(i * parts.run, parts.nb),
-                              min((i + 1) * parts.run, parts.nb), info + i, parts.np, known,
-                              blocks);
+    auto score = [&](auto one_page) {
+      score_run<T, D, NT, true, decltype(one_page)::value>(
+          P, sc, sq, b, hg, len, min(i * parts.run, parts.nb), min((i + 1) * parts.run, parts.nb),
+          info + i, parts.np, known, blocks);
+    };
+    if (P.page_size % 16 == 0) score(std::true_type());
+    else score(std::false_type());
   } else {
     asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
     if (raw_len != 0 && rank == 0 && hg == 0 && tid == 0)

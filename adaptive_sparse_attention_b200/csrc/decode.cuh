@@ -755,11 +755,30 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
   // tau: for beta >= 1 by the steps of norm_step from the lower bound, until it has settled
   // (n_iter does not enter); for beta < 1, where the norm is not convex, by the bracketed search
   // of the attention passes.
+  // A list of up to 32 candidates (quick) is held one per lane, and their values' places are looked
+  // up while tau is found.
   float tau = 0.f;
+  int n_live = 0;  // candidates with p > 0
+  const int32_t* table = P.tables + b * P.table_stride;
+  auto value_row = [&](float2 x) -> int64_t {  // offset of the value of list entry x
+    const int key = min(static_cast<unsigned>(__float_as_int(x.y)),
+                        static_cast<unsigned>(len - 1));
+    const int blk = key / P.page_size, page = table[blk];
+    return (static_cast<unsigned>(page) < static_cast<unsigned>(P.num_pages) ? page : 0) *
+               P.page_stride +
+           (key - blk * P.page_size) * P.slot_stride;
+  };
+  const bool quick = solo && n_list <= 32 && (BK != kBetaGeneral || P.beta >= 1.f);
   if (deal && warp != 0) {
     // waits for the first warp below
-  } else if (solo && n_list <= 32 && (BK != kBetaGeneral || P.beta >= 1.f)) {
-    const float z = lane < n_list ? entry(lane).x : -INFINITY;  // one each: no loop
+  } else if (quick) {
+    float z = -INFINITY;
+    int64_t from = 0;
+    if (lane < n_list) {
+      const float2 x = entry(lane);
+      z = x.x;
+      from = value_row(x);
+    }
     tau = floor;
     for (int it = 0; it < kNewtonSteps; ++it) {
       float s0 = 0.f, s1 = 0.f;
@@ -769,6 +788,10 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
       tau += step;
       if (!(step > 2.f * FLT_EPSILON * fmaxf(fabsf(tau), m - tau))) break;
     }
+    const float p = power<BK>(z - tau, P.beta);
+    const unsigned live = __ballot_sync(kFull, p > 0.f);
+    if (p > 0.f) sm.rows[0][__popc(live & below)] = {from, p};
+    n_live = __popc(live);
   } else if (BK != kBetaGeneral || P.beta >= 1.f) {
     tau = floor;
     for (int it = 0; it < kNewtonSteps; ++it) {
@@ -843,8 +866,7 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
   }
 
   // The entries with p > 0 move to the front of the list, p in the place of z ...
-  int n_live = 0;
-  if (!deal || warp == 0) {
+  if (!quick && (!deal || warp == 0)) {
     for (int e0 = 0; e0 < n_list; e0 += 32) {
       float p = 0.f;
       int key = 0;
@@ -857,9 +879,9 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
       if (p > 0.f) set_entry(n_live + __popc(live & below), p, key);
       n_live += __popc(live);
     }
-    if (deal && lane == 0) sm.count[0] = n_live;
   }
   if (deal) {
+    if (threadIdx.x == 0) sm.count[0] = n_live;
     __syncthreads();
     n_live = sm.count[0];
   } else {
@@ -874,22 +896,18 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
   constexpr int EPL = 16 / sizeof(T);      // elements per lane
   constexpr int U = 4;
   float o[EPL] = {};
-  const int32_t* table = P.tables + b * P.table_stride;
+  const typename JoinSmem<W, C>::Row* rows = quick ? sm.rows[0] + mine : sm.rows[warp];
+  const int row_step = quick ? step : 1;
   const T* vbase = static_cast<const T*>(P.v) + hk * P.head_stride + (lane % LPR) * EPL;
   for (int e0 = 0; e0 < n_live; e0 += 32) {
     const int n = min(32, n_live - e0);
-    if (lane < n) {
-      const float2 x = entry(mine + (e0 + lane) * step);
-      const int key = min(static_cast<unsigned>(__float_as_int(x.y)),
-                          static_cast<unsigned>(len - 1));
-      const int blk = key / P.page_size, page = table[blk];
-      sm.rows[warp][lane].p = x.x;
-      sm.rows[warp][lane].from =
-          (static_cast<unsigned>(page) < static_cast<unsigned>(P.num_pages) ? page : 0) *
-              P.page_stride +
-          (key - blk * P.page_size) * P.slot_stride;
+    if (!quick) {
+      if (lane < n) {
+        const float2 x = entry(mine + (e0 + lane) * step);
+        sm.rows[warp][lane] = {value_row(x), x.x};
+      }
+      __syncwarp();
     }
-    __syncwarp();
     for (int i0 = 0; i0 < n; i0 += RPW * U) {
       uint4 x[U];
       float w[U];
@@ -899,8 +917,8 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
         w[j] = 0.f;
         x[j] = make_uint4(0u, 0u, 0u, 0u);
         if (i < n) {
-          w[j] = sm.rows[warp][i].p;
-          x[j] = load_stream(vbase + sm.rows[warp][i].from);
+          w[j] = rows[i * row_step].p;
+          x[j] = load_stream(vbase + rows[i * row_step].from);
         }
       }
 #pragma unroll

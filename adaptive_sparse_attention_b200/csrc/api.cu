@@ -518,19 +518,21 @@ size_t decode_layout(void* base, int B, int Hq, int Hkv, int max_len, ea::Decode
 }
 
 // Which of the decode kernels serves a call, from its sizes alone (the lengths are on the device).
-// Times on a B200 in us, bf16, d = 128, Hkv = 8, G = 4, alpha = 1.5 with key spikes, all lengths
-// equal unless said otherwise.
+// Times on a B200 in us of a captured call, bf16, d = 128, Hkv = 8, G = 4, alpha = 1.5 with key
+// spikes, all lengths equal unless said otherwise.
 //   cluster: C = 8, 4, 2 or 1 blocks per (request, head group), the most that run all at once (2
-//     blocks per SM).  One launch, about 5 us ahead of the split kernels (B = 1, 1000 keys: 10.4
-//     against 14.5; B = 16, 128 keys: 12.5 against 16.7; 4096 keys: 31 against 37), but a block
+//     blocks per SM).  One launch and no prefix sums, about 2 us ahead of the split kernels, more
+//     for batches (B = 1, 1000 keys: 10.4 against 12.4; B = 16, 128 keys: 14.5 against 16.6, 4096
+//     keys: 31 against 33; B = 33, d = 64, G = 1, lengths to 4096: 25 against 33), but a block
 //     reads about 44 GB/s, so a request much longer than the others, or alone, is late: 1 request
-//     of 131072 keys takes 105 against 56.  So they serve a single request as long as its blocks'
-//     extra time against the 6.3 TB/s of the split kernels is below those 5 us, and a batch if its
-//     longest possible request is read in 12 us.
+//     of 16384 keys takes 17.4 against 16.6, of 131072 98 against 53.  So they serve a single
+//     request as long as its blocks' extra time against the 6.3 TB/s of the split kernels is below
+//     those 2 us, and a batch if its longest possible request is read in 12 us.
 //   join_blocks of the split kernels: up to 148 heads have a cluster of 4 blocks each (B = 4,
-//     lengths to 20000, alpha = 1.333 without spikes: 42 against 45 with one block), up to 1024 a
-//     block each (B = 16, 128 keys: 16.7 against 18.6 with a warp each), more a warp each (B = 64,
-//     128 keys: 20.7 against 31.2 with a block each).
+//     lengths to 20000, alpha = 1.333 without spikes: 37 against 41 with one block; 2 us more with
+//     few candidates), up to 1024 a block each (B = 16, 4096 keys: 33 against 35 with a warp each),
+//     more a warp each (B = 64, 128 keys: 18.6 against 33 with a block each, 16384 keys 342 against
+//     353).
 void choose_decode_kernels(ea::DecodeProblem* P, double row_bytes) {
   const int64_t groups = static_cast<int64_t>(P->B) * P->Hkv * P->head_blocks;
   P->cluster = 0;
@@ -539,7 +541,7 @@ void choose_decode_kernels(ea::DecodeProblem* P, double row_bytes) {
     while (groups * c > 2 * 148) c /= 2;
     const double bytes = P->max_len * row_bytes;  // of the longest request and one kv head
     const double block_us = bytes / (c * 44e3);
-    if (P->B == 1 ? block_us - groups * bytes / 6300e3 <= 5.0 : block_us <= 12.0) P->cluster = c;
+    if (P->B == 1 ? block_us - groups * bytes / 6300e3 <= 2.0 : block_us <= 12.0) P->cluster = c;
   }
   const int64_t heads = static_cast<int64_t>(P->B) * P->Hq;
   P->join_blocks = heads <= 148 ? 4 : heads <= 1024 ? 1 : 0;

@@ -6,8 +6,11 @@
 // with key j in slot j % page_size of page block_tables[b][j / page_size].
 //
 // Two steps.  The scores: every key is read once, and per (request, head) the keys that can carry
-// p > 0 are kept (z > max - 1, since p <= 1 gives tau >= max - 1).  The join: the max over all
-// parts, tau, and o from the values of the keys with z > tau.  A softmax would have to read every
+// p > 0 are kept (z > max - 1, since p <= 1 gives tau >= max - 1).  The join: the max m over all
+// parts, tau, and o from the values of the keys with z > tau.  p is made of the differences z - tau,
+// so the join works with z - m and t = tau - m in [-1, 0), which fp32 resolves whatever the size of
+// the scores (z - m is exact for z >= m / 2 > 0), and adds m only to the tau that it returns: with
+// tau itself 100000 tied keys at z = 30 had a sum of p off by 5% (alpha = 2).  A softmax would have to read every
 // value too; here the values of keys with p = 0 are never read, so the traffic is that of the keys
 // alone unless the supports are wide.  Both steps run in one kernel (decode_cluster_kernel) for
 // small batches, else in two (decode_scores_kernel and a join); choose_decode_kernels picks.
@@ -394,7 +397,7 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
           for (int e = 0; e < 2; ++e) {
             const float top = max_nan(acc[n][e], acc[n][2 + e]);
             own[n][e] = max_nan(own[n][e], top);
-            pass |= top > m[n][e] - 1.f;
+            pass |= top - m[n][e] > -1.f;
           }
         if (__any_sync(kFull, pass)) {
           bool above = false;
@@ -430,7 +433,7 @@ __device__ __forceinline__ void score_run(const DecodeProblem& P,
 #pragma unroll
               for (int r = 0; r < 2; ++r) {
                 const float z = acc[n][2 * r + e];
-                const bool in = z > m[n][e] - 1.f;
+                const bool in = z - m[n][e] > -1.f;  // also where m - 1 rounds to m
                 const unsigned mine = __ballot_sync(kFull, in) & (0x11111111u << t);
                 if (in)
                   cand[n][e][cnt[n][e] + __popc(mine & ((1u << lane) - 1u))] =
@@ -484,7 +487,7 @@ struct JoinSmem {
     float p;
   };
   union {
-    float2 list[W][kList];  // (z or p, key bits)
+    float2 list[W][kList];  // (z - m or p, key bits)
     float o[W][128];        // after the lists: partial sums of o
   };
   float2 all[W > 1 ? kSolo : 1];  // all candidates, when they are few
@@ -520,8 +523,8 @@ __device__ __forceinline__ void share(V* p, V x) {
   }
 }
 
-// One step towards tau from the left, for beta >= 1: Newton's on the norm
-// g(tau) = (sum [z - tau]_+^beta)^(1/beta), which is 1 at tau.  g is convex and falling (a norm of
+// One step towards t from the left, for beta >= 1 (here tau stands for t, z for z - m): Newton's on
+// the norm g(tau) = (sum [z - tau]_+^beta)^(1/beta), which is 1 at tau.  g is convex and falling (a norm of
 // functions that are), so from a point where g >= 1 the iterates rise to the root and never pass
 // it, and g is linear in tau while the support stays and the scores tie, so they are few: 4 or 5
 // on normal scores, 14 at most over a wide sweep of sizes and spreads at beta = 1.  With s0, s1
@@ -564,17 +567,18 @@ struct Parts {
   __device__ __forceinline__ int key0(int i) const { return min(max(i * run - off, 0), nb) * 16; }
 };
 
-// From the maxima of a head's parts: its largest score m, and a lower bound of tau.  The maxima
+// From the maxima of a head's parts: its largest score m, and a lower bound of t = tau - m.  The
+// maxima
 // are scores of the head, and the tau of a part of the keys is at most that of all (more keys only
-// add to the sum), so a few of the steps above on up to 256 of them give a bound far above m - 1:
+// add to the sum), so a few of the steps above on up to 256 of them give a bound far above -1:
 // of 20000 normal scores at alpha = 1.333, 184 lie above tau, 226 above the bound from 64 maxima
 // and 3496 above m - 1.  Where at most half of the parts reach above m - 1 the candidates are few
-// and the bound is m - 1.  (The parts' counts do not enter: in the cluster kernel they depend on
+// and the bound is -1.  (The parts' counts do not enter: in the cluster kernel they depend on
 // the timing, and the bound decides in which order the sums below add.)  Every warp computes both,
 // so that they need no barrier; red: for more than 256 parts, whose maximum the block takes
 // together.
 struct Bounds {
-  float m, floor;
+  float m, floor;  // floor: of t
 };
 template <int BK, int W>
 __device__ __forceinline__ Bounds part_bounds(const DecodeProblem& P, float* red,
@@ -602,10 +606,13 @@ __device__ __forceinline__ Bounds part_bounds(const DecodeProblem& P, float* red
 #pragma unroll
     for (int o = W / 2; o > 0; o >>= 1) r.m = max_nan(r.m, __shfl_xor_sync(kFull, r.m, o));
   }
-  r.floor = r.m - 1.f;
+  r.floor = -1.f;
   int n = 0;  // parts that reach above m - 1
 #pragma unroll
-  for (int j = 0; j < R; ++j) n += __popc(__ballot_sync(kFull, x[j] > r.floor));
+  for (int j = 0; j < R; ++j) {
+    x[j] -= r.m;  // an m of -inf or NaN is refused by the join
+    n += __popc(__ballot_sync(kFull, x[j] > -1.f));
+  }
   if (2 * n > min(np, 32 * R) && (BK != kBetaGeneral || P.beta >= 1.f)) {
     for (int it = 0; it < 3; ++it) {
       float s0 = 0.f, s1 = 0.f;
@@ -615,8 +622,8 @@ __device__ __forceinline__ Bounds part_bounds(const DecodeProblem& P, float* red
       warp_sum2(s0, s1);
       r.floor += norm_step<BK>(s0, s1, P.beta);
     }
-    r.floor -= 4.f * FLT_EPSILON * (fabsf(r.m) + 1.f);  // the steps' rounding
-    r.floor = fmaxf(r.floor, r.m - 1.f);
+    // the steps' rounding: s0 and s1 add 8 terms and 5 partial sums, 13 units of 2^-24 each
+    r.floor = fmaxf(r.floor - 16.f * FLT_EPSILON, -1.f);
   }
   return r;
 }
@@ -646,8 +653,8 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
   };
   if (!(m > -INFINITY)) return undefined();  // a NaN, or every score -inf: p is not defined
 
-  // Each warp compacts the entries above the bound of a contiguous range of parts, in order: the
-  // first kList into shared memory, the others back to the front of the range (an entry only moves
+  // Each warp compacts the entries above the bound of a contiguous range of parts, in order and as
+  // (z - m, key): the first kList into shared memory, the others back to the front of the range (an entry only moves
   // forward, over places that the warp has read already, since it reads them in order).
   int2* cand = P.cand + row * P.cand_stride;
   const int i_end = (me + 1) * np / kAll;
@@ -662,7 +669,7 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
     if (i0 + lane < i_end) {
       const int2 x = parts.part(i0 + lane);
       base = parts.key0(i0 + lane);
-      if (__int_as_float(x.y) > floor)
+      if (__int_as_float(x.y) - m > floor)
         n = min(max(x.x, 0), min(parts.run, parts.nb - (base >> 4)) * 16);
     }
     const int chunks = (n + 31) >> 5;
@@ -692,14 +699,13 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
       }
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const bool in = __int_as_float(x[j].x) > floor;
+        const float z = __int_as_float(x[j].x) - m;
+        const bool in = z > floor;
         const unsigned bal = __ballot_sync(kFull, in);
         const int at = n_list + __popc(bal & below);
         if (in) {
-          if (at < kList)
-            sm.list[warp][at] = make_float2(__int_as_float(x[j].x), __int_as_float(x[j].y));
-          else
-            spill[at - kList] = x[j];
+          if (at < kList) sm.list[warp][at] = make_float2(z, __int_as_float(x[j].y));
+          else spill[at - kList] = make_int2(__float_as_int(z), x[j].y);
         }
         n_list += __popc(bal);
       }
@@ -739,7 +745,7 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
     }
   }
   __syncwarp();
-  if (solo && n_list == 0) return undefined();  // |m| >= 2^23: m - 1 is m in fp32
+  if (solo && n_list == 0) return undefined();  // only where another call writes the workspace
   const bool deal = W > 1 && solo;
   float2* list = deal ? sm.all : sm.list[warp];
   auto entry = [&](int e) {
@@ -752,7 +758,7 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
     else spill[e - kList] = make_int2(__float_as_int(z), key);
   };
 
-  // tau: for beta >= 1 by the steps of norm_step from the lower bound, until it has settled
+  // tau - m, called tau from here on: for beta >= 1 by the steps of norm_step from the lower bound, until it has settled
   // (n_iter does not enter); for beta < 1, where the norm is not convex, by the bracketed search
   // of the attention passes.
   // A list of up to 32 candidates (quick) is held one per lane, and their values' places are looked
@@ -786,7 +792,7 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
       warp_sum2(s0, s1);
       const float step = norm_step<BK>(s0, s1, P.beta);
       tau += step;
-      if (!(step > 2.f * FLT_EPSILON * fmaxf(fabsf(tau), m - tau))) break;
+      if (!(step > 2.f * FLT_EPSILON * fabsf(tau))) break;
     }
     const float p = power<BK>(z - tau, P.beta);
     const unsigned live = __ballot_sync(kFull, p > 0.f);
@@ -825,11 +831,11 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
       }
       const float step = norm_step<BK>(s0, s1, P.beta);
       tau += step;
-      if (!(step > 2.f * FLT_EPSILON * fmaxf(fabsf(tau), m - tau))) break;
+      if (!(step > 2.f * FLT_EPSILON * fabsf(tau))) break;
     }
   } else {
     Search sr;
-    sr.init(m, len, P.alpha);
+    sr.init(0.f, len, P.alpha);
     for (int it = 0; it < P.n_iter; ++it) {
       float s0 = 0.f, s1 = 0.f, s2 = 0.f;
       for (int e = lane; e < n_list; e += 32) {
@@ -956,7 +962,7 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
         store_elem(out, i, s);
       }
   }
-  if (rank == 0 && tid == 0) P.tau[row] = tau;
+  if (rank == 0 && tid == 0) P.tau[row] = m + tau;
 }
 
 // o and tau of a request without keys (o = 0, tau = +inf) or with a length out of range (NaN)
@@ -1120,7 +1126,7 @@ __device__ __forceinline__ void join_many(const DecodeProblem& P, ManySmem& sm, 
     if (DEFER)
       for (int i = lane; i < r.parts.np; i += 32) {
         const int2 x = r.parts.part(i);
-        if (__int_as_float(x.y) > bound.floor) n += x.x;
+        if (__int_as_float(x.y) - bound.m > bound.floor) n += x.x;
       }
     if (DEFER && __reduce_add_sync(kFull, n) > kWarpEntries) {
       if (lane == 0) {

@@ -334,9 +334,9 @@ size_t entmax_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int max_len);
  *   seq_lens int32 [B], at most max_len <= W * page_size.
  *   n_iter: steps of the tau search for alpha > 2; for alpha <= 2 it runs until tau has settled.
  * A request of length 0 (an unused row of the batch) has out = 0 and tau = +inf.  Only the values
- * of keys with p > 0 are read.  A score that is NaN or +inf, or scores beyond 2^23 (where fp32
- * resolves no p), make out and tau of their (request, head) NaN.  A length outside [0, max_len] or
- * a page outside [0, num_pages) makes those of the request NaN and latches ENTMAX_ATTN_ERANGE in
+ * of keys with p > 0 are read.  p is computed from differences of the scores, so a common shift of
+ * them costs it nothing beyond the scores' own rounding.  A score that is NaN or +inf, or scores that
+ * are all -inf, make out and tau of their (request, head) NaN.  A length outside [0, max_len] or a page outside [0, num_pages) makes those of the request NaN and latches ENTMAX_ATTN_ERANGE in
  * the status word; nothing outside the cache is read.
  * workspace: device memory of entmax_attn_decode_workspace_bytes(...), 256-byte aligned, owned by
  * the caller, needed until the call's work has completed; its contents need not be initialised or

@@ -785,7 +785,6 @@ int entmax_attn_decode(const void* q, long long q_stride_b, long long q_stride_h
   P.table_stride = table_stride;
   P.num_pages = num_pages;
   P.page_size = page_size;
-  P.n_iter = n_iter;
   P.alpha = alpha;
   P.beta = beta;
   P.c = static_cast<float>((a - 1.0) / std::sqrt(static_cast<double>(d)));

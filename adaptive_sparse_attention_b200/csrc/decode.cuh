@@ -7,13 +7,15 @@
 //
 // Two steps.  The scores: every key is read once, and per (request, head) the keys that can carry
 // p > 0 are kept (z > max - 1, since p <= 1 gives tau >= max - 1).  The join: the max m over all
-// parts, tau, and o from the values of the keys with z > tau.  p is made of the differences z - tau,
-// so the join works with z - m and t = tau - m in [-1, 0), which fp32 resolves whatever the size of
-// the scores (z - m is exact for z >= m / 2 > 0), and adds m only to the tau that it returns: with
-// tau itself 100000 tied keys at z = 30 had a sum of p off by 5% (alpha = 2).  A softmax would have to read every
+// parts, tau, and o from the values of the keys with z > tau.  A softmax would have to read every
 // value too; here the values of keys with p = 0 are never read, so the traffic is that of the keys
 // alone unless the supports are wide.  Both steps run in one kernel (decode_cluster_kernel) for
 // small batches, else in two (decode_scores_kernel and a join); choose_decode_kernels picks.
+//
+// p is made of the differences z - tau, so the join works with z - m and t = tau - m in [-1, 0),
+// which fp32 resolves whatever the size of the scores (z - m is exact for z >= m / 2 > 0), and adds
+// m only to the tau that it returns: with tau itself 100000 tied keys at z = 30 had a sum of p off
+// by 5% (alpha = 2).
 //
 // What bounds it: HBM reads of the keys; for small calls the chain of dependent reads (length,
 // page, keys, candidates, page, value), about 9 us.  In the split kernels the cache is cut in units
@@ -38,7 +40,8 @@ namespace {
 
 constexpr int kScoreThreads = 128;
 constexpr int kScoreWarps = kScoreThreads / 32;
-constexpr int kNewtonSteps = 64;  // a bound that no search reaches
+constexpr int kNewtonSteps = 64;  // bounds that no search reaches
+constexpr int kHalvings = 64;
 constexpr int kSolo = 256;  // candidates of a head that one warp takes alone
 constexpr unsigned kFull = 0xffffffffu;
 
@@ -493,7 +496,6 @@ struct JoinSmem {
   float2 all[W > 1 ? kSolo : 1];  // all candidates, when they are few
   Row rows[W][32];
   float2 sums[2][C * W];
-  float sums2[2][C * W];
   float red[W];
   int count[C * W];
   float co[C > 1 ? C : 1][C > 1 ? 128 : 1];  // the blocks' sums of o
@@ -758,9 +760,10 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
     else spill[e - kList] = make_int2(__float_as_int(z), key);
   };
 
-  // tau - m, called tau from here on: for beta >= 1 by the steps of norm_step from the lower bound, until it has settled
-  // (n_iter does not enter); for beta < 1, where the norm is not convex, by the bracketed search
-  // of the attention passes.
+  // tau - m, called tau from here on: for beta >= 1 by the steps of norm_step from the lower bound,
+  // until it has settled; for beta < 1 by bisection, because the sum falls with an infinite slope at
+  // every score, where steps by derivatives stall short of the root (the attention passes' search
+  // left sums of p up to 2000 off).
   // A list of up to 32 candidates (quick) is held one per lane, and their values' places are looked
   // up while tau is found.
   float tau = 0.f;
@@ -834,41 +837,33 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
       if (!(step > 2.f * FLT_EPSILON * fabsf(tau))) break;
     }
   } else {
-    Search sr;
-    sr.init(0.f, len, P.alpha);
-    for (int it = 0; it < P.n_iter; ++it) {
-      float s0 = 0.f, s1 = 0.f, s2 = 0.f;
-      for (int e = lane; e < n_list; e += 32) {
-        const float y = entry(e).x - sr.tau;
-        if (y > 0.f) {
-          float p0, p1, p2;
-          entmax_powers<BK>(y, P.beta, p0, p1, p2);
-          s0 += p0;
-          s1 += p1;
-          s2 += p2;
-        }
-      }
+    // [-1, -n^(1 - alpha)] holds the root: p <= 1, and n keys at most 0 have it at the upper end when
+    // all tie there (moved by the rounding of the power).  Halved until its ends are neighbours, by
+    // the geometric mean while they lie far apart: 24 to 35 steps.
+    float lo = -1.f, hi = -0.9999f * fmaxf(exp2f((1.f - P.alpha) * log2f(len)), FLT_MIN);
+    float over = INFINITY, under = 1.f;  // how far the sum is from 1 at lo and at hi
+    for (int it = 0; it < kHalvings; ++it) {
+      const float mid = lo < 4.f * hi ? -sqrtf(-lo) * sqrtf(-hi) : 0.5f * (lo + hi);
+      if (!(mid > lo && mid < hi)) break;
+      float s0 = 0.f;
+      for (int e = lane; e < n_list; e += 32) s0 += power<BK>(entry(e).x - mid, P.beta);
 #pragma unroll
-      for (int o = 16; o > 0; o >>= 1) {
-        s0 += __shfl_xor_sync(kFull, s0, o);
-        s1 += __shfl_xor_sync(kFull, s1, o);
-        s2 += __shfl_xor_sync(kFull, s2, o);
-      }
+      for (int o = 16; o > 0; o >>= 1) s0 += __shfl_xor_sync(kFull, s0, o);
       if (W > 1 && !solo) {
-        share<C>(&sm.sums[it & 1][me], make_float2(s0, s1));
-        share<C>(&sm.sums2[it & 1][me], s2);
+        share<C>(&sm.sums[it & 1][me], make_float2(s0, 0.f));
         join_sync<W, C>();
-        s0 = s1 = s2 = 0.f;
-        for (int i = 0; i < kAll; ++i) {
-          s0 += sm.sums[it & 1][i].x;
-          s1 += sm.sums[it & 1][i].y;
-          s2 += sm.sums2[it & 1][i];
-        }
+        s0 = 0.f;
+        for (int i = 0; i < kAll; ++i) s0 += sm.sums[it & 1][i].x;
       }
-      sr.step<BK>(s0, s1, s2, P.beta);
-      if (sr.settled()) break;
+      if (s0 > 1.f) {
+        lo = mid;
+        over = s0 - 1.f;
+      } else {
+        hi = mid;
+        under = 1.f - s0;
+      }
     }
-    tau = sr.tau;
+    tau = over < under ? lo : hi;
   }
 
   // The entries with p > 0 move to the front of the list, p in the place of z ...

@@ -139,7 +139,6 @@ struct DecodeProblem {
   int num_pages, page_size;
   int B, Hq, Hkv, G, max_len;
   int head_blocks, heads_per_block;  // query heads of a kv head are scored 8 or 16 at a time
-  int n_iter;
   float alpha, beta, c;
   int score_warps;
   int cluster;      // blocks per cluster of the one-launch kernel; 0 = the split kernels

@@ -106,11 +106,11 @@ def entmax_attn_decode(q, k_cache, v_cache, block_tables, seq_lens, alpha: float
 
     q [B, Hq, d] or [B, Hq, 1, d] in the cache's dtype, unit-stride rows, batch and head strides in
     multiples of 16 bytes; block_tables int32 [B, W]; seq_lens int32 [B], at most max_len (default:
-    W * page_size; a smaller bound needs less workspace).  n_iter bounds the search's steps for
-    alpha > 2; for alpha <= 2 it runs until tau has settled.  Returns (out, tau): out like q, tau
-    fp32 with q's leading shape.  A request of length 0 gets out = 0 and tau = +inf.  workspace: a
-    buffer of decode_workspace_bytes(B, Hq, Hkv, max_len), allocated here unless given; calls that
-    overlap on the device need one each."""
+    W * page_size; a smaller bound needs less workspace).  n_iter is checked but has no effect (the
+    forward pass's parameter): tau is searched until it has settled.  Returns (out, tau): out like
+    q, tau fp32 with q's leading shape.  A request of length 0 gets out = 0 and tau = +inf.
+    workspace: a buffer of decode_workspace_bytes(B, Hq, Hkv, max_len), allocated here unless given;
+    calls that overlap on the device need one each."""
     if stream is not None:
         with _on(stream, k_cache.device):
             return entmax_attn_decode(q, k_cache, v_cache, block_tables, seq_lens, alpha, n_iter,

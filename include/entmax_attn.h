@@ -332,7 +332,9 @@ size_t entmax_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int max_len);
  *   q: element e of (b, h) at b * q_stride_b + h * q_stride_h + e (strides in elements, multiples of
  *      16 bytes); out [B, Hq, d] contiguous, q's dtype; tau fp32 [B, Hq].
  *   seq_lens int32 [B], at most max_len <= W * page_size.
- *   n_iter: steps of the tau search for alpha > 2; for alpha <= 2 it runs until tau has settled.
+ *   n_iter: checked, without effect (the forward pass's parameter): tau is searched until it has
+ *      settled.  alpha > 2: p rises from 0 with an infinite slope, so p near 0 is good to
+ *      (rounding of a score)^(1 / (alpha - 1)); tau is resolved down to max - 2^-126.
  * A request of length 0 (an unused row of the batch) has out = 0 and tau = +inf.  Only the values
  * of keys with p > 0 are read.  p is computed from differences of the scores, so a common shift of
  * them costs it nothing beyond the scores' own rounding.  A score that is NaN or +inf, or scores that

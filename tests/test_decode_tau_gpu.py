@@ -115,3 +115,34 @@ def test_a_common_shift_of_the_scores_changes_nothing(dtype, alpha, max_len):
     tol = err + (want + err) * torch.finfo(DT[dtype]).eps / 2
     for out, _ in outs:
         assert np.all(np.abs(out[0, 0].double().cpu().numpy() - want) <= tol)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("alpha", [2.1, 3.0, 4.0, 8.0])
+@pytest.mark.parametrize("n,heads,max_len", [(1, 4, None), (2, 4, None), (50, 8, None),
+                                             (1000, 8, None), (20000, 4, None), (20000, 160, None),
+                                             (1000, 8, 200000)])
+@pytest.mark.parametrize("spread", [0.0, 0.01, 0.3, 1.0, 5.0])
+def test_alpha_above_two_settles_by_itself(dtype, alpha, n, heads, max_len, spread, oracle):
+    """For alpha > 2 the sum of the p has a cusp at every score (p rises with an infinite slope), on
+    which steps by derivatives stall or stop short of the root.  The default n_iter; the scores'
+    standard deviation is `spread` (every score ties at 0).  Bounds: oracle.paged.decode_bounds."""
+    from oracle import paged
+    d, P = 64, 16
+    a32 = orc.alpha_as_float32(alpha)
+    g = torch.Generator().manual_seed(n + heads)
+    pages = -(-n // P)
+    W = -(-(max_len or n) // P)
+    kc, vc = (torch.randn(pages, 1, P, d, generator=g).to(DT[dtype]) for _ in range(2))
+    q = (torch.randn(1, heads, d, generator=g) * (spread / (a32 - 1.0))).to(DT[dtype])
+    table = np.full((1, W), -1)
+    table[0, :pages] = np.arange(pages)
+    out, tau = ea.entmax_attn_decode(
+        q.cuda(), kc.cuda(), vc.cuda(), torch.from_numpy(table).int().cuda(),
+        torch.tensor([n], dtype=torch.int32).cuda(), alpha, max_len=max_len)
+    rows = slice(0, 8)  # of the heads: the oracle's time
+    qd, kd, vd = (x.double().numpy() for x in (q[:, rows], kc, vc))
+    o, t = paged.decode(qd, kd, vd, table, [n], a32)
+    bo, bt = paged.decode_bounds(qd, kd, vd, table, [n], a32, t, torch.finfo(DT[dtype]).eps)
+    assert np.all(np.abs(tau[:, rows].double().cpu().numpy() - t) <= bt)
+    assert np.all(np.abs(out[:, rows].double().cpu().numpy() - o) <= bo)

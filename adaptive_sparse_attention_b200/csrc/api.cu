@@ -659,8 +659,8 @@ int entmax_attn_page_tables(const int32_t* lens, const int32_t* new_lens,
                             int32_t* lens_out, int32_t* cu_new, int32_t* free_next,
                             cudaStream_t stream) {
   if (!lens || !new_lens || (!free_pages && n_free != 0) || !free_start || !block_tables ||
-      !slots || !lens_out || !cu_new || !free_next || n_free < 0 || W < 1 || B < 1 ||
-      B > ea::kMaxRequests || table_stride < W || page_size < 1 || n_new < 1 ||
+      (!slots) != (n_new == 0) || !lens_out || !cu_new || !free_next || n_free < 0 || W < 1 ||
+      B < 1 || B > ea::kMaxRequests || table_stride < W || page_size < 1 || n_new < 0 ||
       (padded != 0 && padded != 1) || lens_out == lens || lens_out == new_lens ||
       free_next == free_start || static_cast<int64_t>(B) * W >= (int64_t(1) << 31))
     return ENTMAX_ATTN_EINVAL;
@@ -746,7 +746,9 @@ int entmax_attn_decode(const void* q, long long q_stride_b, long long q_stride_h
                        const int32_t* seq_lens, void* out, float* tau, void* workspace,
                        size_t workspace_bytes, int B, int Hq, int Hkv, int max_len, int d,
                        float alpha, int n_iter, int dtype, cudaStream_t stream) {
-  if (!q || !block_tables || !seq_lens || !out || !tau || !workspace || W < 1 ||
+  // no request holds a key: nothing but the outputs is written
+  const bool no_keys = max_len == 0 && !workspace && workspace_bytes == 0;
+  if (!q || !block_tables || !seq_lens || !out || !tau || (!workspace && !no_keys) || W < 1 ||
       table_stride < W || q_stride_b < 0 || q_stride_h < 0 || !std::isfinite(alpha) ||
       !(alpha > 1.f) || n_iter < 1 || n_iter > 1000)
     return ENTMAX_ATTN_EINVAL;
@@ -760,13 +762,14 @@ int entmax_attn_decode(const void* q, long long q_stride_b, long long q_stride_h
   const float beta = static_cast<float>(1.0 / (a - 1.0));
   if (!std::isfinite(beta)) return ENTMAX_ATTN_EINVAL;
   ea::DecodeProblem P = {};
-  const size_t need = decode_layout(workspace, B, Hq, Hkv, max_len, &P);
-  if (need == 0) return ENTMAX_ATTN_EINVAL;
+  const size_t need = decode_layout(workspace, B, Hq, Hkv, no_keys ? 1 : max_len, &P);
+  if (need == 0 || (no_keys && static_cast<int64_t>(Hkv) * P.head_blocks > 65535))
+    return ENTMAX_ATTN_EINVAL;
   if (!aligned16(q) || !aligned16(out) || (reinterpret_cast<uintptr_t>(block_tables) & 3u) ||
       (reinterpret_cast<uintptr_t>(seq_lens) & 3u) || (reinterpret_cast<uintptr_t>(tau) & 3u) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return ENTMAX_ATTN_EALIGN;
-  if (workspace_bytes < need) return ENTMAX_ATTN_ENOMEM;
+  if (workspace_bytes < need && !no_keys) return ENTMAX_ATTN_ENOMEM;
   int err = ENTMAX_ATTN_OK;
   P.status = status_ptr(&err);
   if (!P.status) return err;
@@ -789,6 +792,10 @@ int entmax_attn_decode(const void* q, long long q_stride_b, long long q_stride_h
   P.beta = beta;
   P.c = static_cast<float>((a - 1.0) / std::sqrt(static_cast<double>(d)));
   choose_decode_kernels(&P, static_cast<double>(d * esz));
+  if (no_keys) {  // the cluster kernel writes every row before it would touch the workspace
+    P.max_len = 0;
+    P.cluster = 1;
+  }
   cudaError_t e;
   if (dtype == ENTMAX_ATTN_FP32)
     e = d == 64 ? ea::launch_decode_fp32_64(P, stream) : ea::launch_decode_fp32_128(P, stream);

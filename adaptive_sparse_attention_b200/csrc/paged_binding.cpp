@@ -54,7 +54,7 @@ int int32(PyObject* o, const char* name) {
 const at::Tensor& ints(PyObject* o, const char* name, int dim, at::Device dev) {
   const at::Tensor& t = tensor(o, name);
   if (!t.is_cuda() || t.device() != dev || t.scalar_type() != at::kInt || t.dim() != dim ||
-      (t.size(dim - 1) > 1 && t.stride(dim - 1) != 1) || t.size(dim - 1) > INT32_MAX)
+      (t.size(dim - 1) > 1 && t.stride(dim - 1) != 1 && t.numel() > 0) || t.size(dim - 1) > INT32_MAX)
     refuse("%s must be a %d-D int32 CUDA tensor with a unit-stride last dimension, on the device "
            "of the others", name, dim);
   return t;
@@ -177,7 +177,7 @@ PyObject* page_tables(PyObject*, PyObject* const* a, Py_ssize_t n) {
         static_cast<const int32_t*>(start.const_data_ptr()),
         static_cast<int32_t*>(tables.mutable_data_ptr()), B > 1 ? tables.stride(0) : W,
         static_cast<int>(W), static_cast<int>(B), page,
-        static_cast<int64_t*>(slots.mutable_data_ptr()), n_new, padded,
+        n_new ? static_cast<int64_t*>(slots.mutable_data_ptr()) : nullptr, n_new, padded,
         static_cast<int32_t*>(lens_out.mutable_data_ptr()),
         static_cast<int32_t*>(cu.mutable_data_ptr()),
         static_cast<int32_t*>(next.mutable_data_ptr()),
@@ -229,7 +229,8 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const at::Tensor& q = tensor(a[0], "q");
     const int64_t dim = q.dim();
     if (!(dim == 3 || (dim == 4 && q.size(2) == 1)) || q.size(dim - 1) != c.d ||
-        q.scalar_type() != c.k.scalar_type() || q.device() != c.dev || q.stride(dim - 1) != 1)
+        q.scalar_type() != c.k.scalar_type() || q.device() != c.dev ||
+        (q.stride(dim - 1) != 1 && q.numel() > 0))
       refuse("q must be [B, Hq, d] or [B, Hq, 1, d] with the cache's head size, dtype and device, "
              "and unit-stride rows");
     const int64_t B = q.size(0), Hq = q.size(1);
@@ -243,19 +244,22 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int n_iter = int32(a[6], "n_iter");
     const int64_t bound = a[7] == Py_None ? W * c.page : integer(a[7]);
     if (bound > INT32_MAX) refuse("max_len must be below 2^31");
-    const int max_len = static_cast<int>(bound < 0 ? 0 : bound);
+    if (bound < 0) refuse("max_len must not be negative");
+    const int max_len = static_cast<int>(bound);
     const c10::cuda::CUDAGuard on(c.dev);
     const at::Tensor out = output(a[8], "out", q.sizes(), q.scalar_type(), c.dev);
     const at::Tensor tau = output(a[9], "tau", q.sizes().slice(0, dim - 1), at::kFloat, c.dev);
+    if (B == 0) return Py_BuildValue("(NN)", THPVariable_Wrap(out), THPVariable_Wrap(tau));
+    const bool no_keys = max_len == 0;  // takes no workspace
     at::Tensor own;
-    if (a[10] == Py_None) {
+    if (a[10] == Py_None && !no_keys) {
       const size_t need = entmax_attn_decode_workspace_bytes(
           static_cast<int>(B), static_cast<int>(Hq), c.heads, max_len);
       if (need == 0) return PyLong_FromLong(ENTMAX_ATTN_EINVAL);
       own = empty({static_cast<int64_t>(need)}, at::kByte, c.dev);
     }
     const at::Tensor& ws = a[10] == Py_None ? own : tensor(a[10], "workspace");
-    if (ws.device() != c.dev || !ws.is_contiguous())
+    if (ws.defined() && (ws.device() != c.dev || !ws.is_contiguous()))
       refuse("workspace must be a contiguous buffer on the cache's device");
     const int rc = entmax_attn_decode(
         q.const_data_ptr(), B > 1 ? q.stride(0) : 0, Hq > 1 ? q.stride(1) : 0,
@@ -263,7 +267,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
         static_cast<const int32_t*>(tables.const_data_ptr()), B > 1 ? tables.stride(0) : W,
         static_cast<int>(W), static_cast<const int32_t*>(lens.const_data_ptr()),
         out.mutable_data_ptr(), static_cast<float*>(tau.mutable_data_ptr()),
-        ws.mutable_data_ptr(), ws.nbytes(), static_cast<int>(B), static_cast<int>(Hq), c.heads,
+        no_keys ? nullptr : ws.mutable_data_ptr(), no_keys ? 0 : ws.nbytes(), static_cast<int>(B), static_cast<int>(Hq), c.heads,
         max_len, c.d, static_cast<float>(alpha), n_iter, c.dtype,
         c10::cuda::getCurrentCUDAStream(c.dev.index()).stream());
     if (rc != ENTMAX_ATTN_OK) return PyLong_FromLong(rc);

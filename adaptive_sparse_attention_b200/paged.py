@@ -59,7 +59,7 @@ def page_tables(lens, new_lens, free_pages, free_start, block_tables, page_size:
     cu_new, free_next): slots int64 [n_new], the new tokens packed in request order and -1 behind
     the last, or with padded=True [B, n_new], -1 for t >= new_lens[b]; lens_out int32 [B]; cu_new
     int32 [B + 1], the prefix sums of new_lens (the cu_seqlens of the packed forward pass); free_next
-    int32 [1].  A request that does not fit keeps its length and gets slots of -1 (see
+    int32 [1].  B is at least 1; n_new may be 0.  A request that does not fit keeps its length and gets slots of -1 (see
     include/entmax_attn.h).  The outputs may be given; lens_out and free_next may not be the
     inputs themselves.  Where none of lens_out, cu_new and free_next is, they share one storage."""
     if stream is not None:
@@ -94,7 +94,7 @@ def decode_workspace_bytes(B: int, Hq: int, Hkv: int, max_len: int) -> int:
 def alloc_decode_workspace(q, k_cache, max_len: int):
     """Workspace of entmax_attn_decode for q's batch and requests of up to max_len tokens."""
     n = decode_workspace_bytes(q.shape[0], q.shape[1], k_cache.shape[1], max_len)
-    if n == 0:
+    if n == 0 and q.shape[0] != 0 and max_len != 0:  # without requests or keys none is needed
         raise ValueError("bad sizes for a decode workspace")
     return torch.empty(n, dtype=torch.uint8, device=q.device)
 
@@ -106,11 +106,11 @@ def entmax_attn_decode(q, k_cache, v_cache, block_tables, seq_lens, alpha: float
 
     q [B, Hq, d] or [B, Hq, 1, d] in the cache's dtype, unit-stride rows, batch and head strides in
     multiples of 16 bytes; block_tables int32 [B, W]; seq_lens int32 [B], at most max_len (default:
-    W * page_size; a smaller bound needs less workspace).  n_iter is checked but has no effect (the
-    forward pass's parameter): tau is searched until it has settled.  Returns (out, tau): out like
-    q, tau fp32 with q's leading shape.  A request of length 0 gets out = 0 and tau = +inf.
-    workspace: a buffer of decode_workspace_bytes(B, Hq, Hkv, max_len), allocated here unless given;
-    calls that overlap on the device need one each."""
+    W * page_size; a smaller bound needs less workspace; 0 where all rows are unused).  n_iter is
+    checked but has no effect (the forward pass's parameter): tau is searched until it has settled.
+    Returns (out, tau): out like q, tau fp32 with q's leading shape.  A request of length 0 gets
+    out = 0 and tau = +inf.  workspace: a buffer of decode_workspace_bytes(B, Hq, Hkv, max_len),
+    allocated here unless given; calls that overlap on the device need one each."""
     if stream is not None:
         with _on(stream, k_cache.device):
             return entmax_attn_decode(q, k_cache, v_cache, block_tables, seq_lens, alpha, n_iter,

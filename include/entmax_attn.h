@@ -288,7 +288,8 @@ int entmax_attn_route_chunks(const void* q, const void* summaries, float* pi, fl
  * is written.
  *   slots:  padded = 0: int64 [n_new], the new tokens of all requests packed in order (request b's
  *           start at cu_new[b]), -1 behind the last; padded = 1: int64 [B][n_new], token t of
- *           request b at [b][t], -1 for t >= new_lens[b].
+ *           request b at [b][t], -1 for t >= new_lens[b].  NULL with n_new = 0: a step without
+ *           tokens.
  *   lens_out int32 [B]: the lengths after the step.  cu_new int32 [B + 1]: prefix sums of new_lens.
  *   free_next int32 [1]: free_start after the step.
  * A request that does not fit keeps its length, takes no page, and its tokens get slot -1: one
@@ -298,7 +299,7 @@ int entmax_attn_route_chunks(const void* q, const void* summaries, float* pi, fl
  * slot -1.  The sums of new_lens and B * W must stay below 2^31.
  * Outputs may not overlap inputs (block_tables is both).  Device pointers, aligned to their
  * element size; asynchronous on `stream`.  Returns ENTMAX_ATTN_OK, ENTMAX_ATTN_EINVAL (null pointer,
- * size < 1, n_free < 0, B > 8192, table_stride < W, padded not 0/1, lens_out == lens or new_lens,
+ * size < 1 except n_new = 0 with slots NULL, n_free < 0, B > 8192, table_stride < W, padded not 0/1, lens_out == lens or new_lens,
  * free_next == free_start), ENTMAX_ATTN_EALIGN or ENTMAX_ATTN_ECUDA. */
 int entmax_attn_page_tables(const int32_t* lens, const int32_t* new_lens,
                             const int32_t* free_pages, int n_free, const int32_t* free_start,
@@ -324,14 +325,15 @@ int entmax_attn_paged_append(const void* k, const void* v, long long stride_b, l
                              int T, int d, int dtype, cudaStream_t stream);
 
 /* Bytes of workspace entmax_attn_decode needs for requests of up to max_len tokens; 0 on bad
- * sizes. */
+ * sizes and for max_len = 0. */
 size_t entmax_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int max_len);
 
 /* alpha-entmax attention of one new token per request over its paged keys and values: the forward
  * pass for q of one row per (request, head), which sees all seq_lens[b] keys.
  *   q: element e of (b, h) at b * q_stride_b + h * q_stride_h + e (strides in elements, multiples of
  *      16 bytes); out [B, Hq, d] contiguous, q's dtype; tau fp32 [B, Hq].
- *   seq_lens int32 [B], at most max_len <= W * page_size.
+ *   seq_lens int32 [B], at most max_len <= W * page_size.  max_len = 0, for a batch of unused rows,
+ *      takes no workspace: NULL and 0 bytes (and at most 65535 kv heads of 16 query heads each).
  *   n_iter: checked, without effect (the forward pass's parameter): tau is searched until it has
  *      settled.  alpha > 2: p rises from 0 with an infinite slope, so p near 0 is good to
  *      (rounding of a score)^(1 / (alpha - 1)); tau is resolved down to max - 2^-126.

@@ -1,0 +1,99 @@
+"""The paged-cache operators at the edges of what they accept: steps without tokens, keys or
+requests."""
+import random
+
+import numpy as np
+import pytest
+import torch
+
+import adaptive_sparse_attention_b200 as ea
+from adaptive_sparse_attention_b200 import _native
+from oracle import paged
+
+pytestmark = pytest.mark.gpu
+DT = {"bf16": torch.bfloat16, "fp32": torch.float32}
+
+
+def i32(x):
+    return torch.as_tensor(np.asarray(x), dtype=torch.int32).cuda()
+
+
+def check_tables(lens, new, free, start, tables, page, n_new, padded, **kw):
+    want = paged.page_tables(lens, new, free, start, tables.cpu().numpy(), page, n_new, padded)
+    got = ea.page_tables(i32(lens), i32(new), i32(free), i32([start]), tables, page, n_new, padded,
+                         **kw)
+    for name, a, b in zip(("tables", "slots", "lens", "cu", "next"), want, (tables,) + got):
+        assert tuple(b.shape) in (np.shape(a), (1,)), name
+        assert np.array_equal(a, b.cpu().numpy().reshape(np.shape(a))), name
+    return got
+
+
+@pytest.mark.parametrize("padded", [False, True])
+@pytest.mark.parametrize("B", [1, 5, 1000])
+def test_tables_of_a_step_without_tokens(B, padded):
+    """n_new = 0: lengths, offsets and the start are passed on; a request with new tokens all the
+    same does not fit."""
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 40, size=B)
+    tables = i32(rng.integers(0, 99, size=(B, 4)))
+    before = tables.clone()
+    for new in (np.zeros(B, dtype=int), (rng.random(B) < 0.5).astype(int)):
+        check_tables(lens, new, [4, 5, 6], 1, tables, 16, 0, padded)
+        check_tables(lens, new, [4, 5, 6], 1, tables, 16, 0, padded,
+                     slots=torch.empty((B, 0) if padded else 0, dtype=torch.int64, device="cuda"))
+    assert torch.equal(tables, before)
+
+
+def unused_batch(B, Hq, Hkv, d, dtype, W=3):
+    q = torch.randn(B, Hq, d).to(DT[dtype]).cuda()
+    kc, vc = (torch.randn(4, Hkv, 16, d).to(DT[dtype]).cuda() for _ in range(2))
+    return q, kc, vc, i32(np.full((B, W), -1)), i32([0] * B)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("B,Hq,Hkv,d", [(1, 1, 1, 64), (3, 40, 2, 128), (700, 8, 8, 64)])
+@pytest.mark.parametrize("given", [False, True])
+def test_decode_of_a_batch_of_unused_rows(dtype, B, Hq, Hkv, d, given):
+    """max_len = max(seq_lens) = 0, with a workspace or without."""
+    q, kc, vc, tables, lens = unused_batch(B, Hq, Hkv, d, dtype)
+    ws = ea.alloc_decode_workspace(q, kc, 0) if given else None
+    out, tau = ea.entmax_attn_decode(q, kc, vc, tables, lens, 1.5, max_len=0, workspace=ws)
+    assert out.shape == q.shape and (out == 0).all()
+    assert torch.isposinf(tau).all()
+    assert ea.status() == 0
+
+
+def test_decode_reports_a_length_above_a_bound_of_zero():
+    q, kc, vc, tables, lens = unused_batch(4, 2, 1, 64, "bf16")
+    tables[2, 0] = 1
+    lens[2] = 1
+    lens[3] = -1
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device="cuda")
+    out, tau = ea.entmax_attn_decode(q, kc, vc, tables, lens, 1.5, max_len=0, workspace=ws)
+    assert ea.status() == _native.ERANGE and ea.status() == 0
+    assert torch.isnan(out[2:]).all() and torch.isnan(tau[2:]).all()
+    assert (out[:2] == 0).all() and torch.isposinf(tau[:2]).all()
+
+
+def test_decode_of_no_requests():
+    q, kc, vc, tables, lens = unused_batch(0, 4, 2, 64, "bf16")
+    for x in (q, q.unsqueeze(2)):
+        out, tau = ea.entmax_attn_decode(x, kc, vc, tables, lens, 1.5,
+                                         workspace=ea.alloc_decode_workspace(x, kc, 48))
+        assert out.shape == x.shape and tau.shape == x.shape[:-1] and tau.dtype == torch.float32
+    with pytest.raises(ValueError):
+        ea.entmax_attn_decode(q.float(), kc, vc, tables, lens)
+
+
+def test_sizes_that_are_wrong_are_still_refused():
+    q, kc, vc, tables, lens = unused_batch(2, 4, 2, 64, "bf16")
+    with pytest.raises((ValueError, _native.EntmaxAttnError)):
+        ea.entmax_attn_decode(q, kc, vc, tables, lens, 1.5, max_len=-1)
+    with pytest.raises((ValueError, _native.EntmaxAttnError)):
+        ea.entmax_attn_decode(q[:, :3], kc, vc, tables, lens, 1.5, max_len=0)
+    with pytest.raises((ValueError, _native.EntmaxAttnError)):
+        ea.entmax_attn_decode(q, kc, vc, tables, lens, 0.5, max_len=0)
+    with pytest.raises(ValueError):
+        ea.alloc_decode_workspace(q, kc, -1)
+    with pytest.raises((ValueError, _native.EntmaxAttnError)):
+        ea.page_tables(lens, lens, lens, lens[:1], tables, 16, -1)

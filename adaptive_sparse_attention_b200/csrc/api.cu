@@ -489,7 +489,8 @@ int check_cache(const void* k, const void* v, long long page_stride, long long h
 // scores; only the candidates (z > running max - 1) are written.  Returns the bytes, 0 on bad
 // sizes.
 size_t decode_layout(void* base, int B, int Hq, int Hkv, int max_len, ea::DecodeProblem* P) {
-  if (B < 1 || B > ea::kMaxRequests || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 1)
+  if (B < 1 || B > ea::kMaxRequests || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || max_len < 1 ||
+      max_len > ea::kMaxKeys)
     return 0;
   P->B = B;
   P->Hq = Hq;

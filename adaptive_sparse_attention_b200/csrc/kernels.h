@@ -124,6 +124,9 @@ cudaError_t launch_paged_append(const PagedAppend& P, int row_bytes, cudaStream_
 
 // One-token attention over the paged cache (entmax_attn_decode); strides in elements.
 constexpr int kDecodeScoreWarps = 148 * 16;  // warps of the score kernel: 16 on each SM
+// Keys of a request: key numbers, rounded up to units of 16 and by what the join reads ahead, fit an
+// int.
+constexpr int kMaxKeys = 0x7fffffff - 4095;
 struct DecodeProblem {
   const void* q;
   const void* k;

@@ -350,8 +350,9 @@ size_t entmax_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int max_len);
  * synchronisation, so it can be captured into a graph and replayed as the lengths grow up to
  * max_len.  Returns ENTMAX_ATTN_OK, ENTMAX_ATTN_EINVAL (null pointer, size < 1, B > 8192,
  * Hq % Hkv != 0, d not 64 or 128, bad stride, max_len > W * page_size, alpha <= 1 or not finite,
- * n_iter outside [1, 1000], bad dtype), ENTMAX_ATTN_EALIGN, ENTMAX_ATTN_ENOMEM (workspace too
- * small) or ENTMAX_ATTN_ECUDA. */
+ * n_iter outside [1, 1000], bad dtype, max_len > 2^31 - 4096, or B * Hkv * ceil(Hq / Hkv / 16) *
+ * ceil(max_len / 16) of 2^31 or more), ENTMAX_ATTN_EALIGN, ENTMAX_ATTN_ENOMEM (workspace too small)
+ * or ENTMAX_ATTN_ECUDA. */
 int entmax_attn_decode(const void* q, long long q_stride_b, long long q_stride_h,
                        const void* k_cache, const void* v_cache, long long page_stride,
                        long long head_stride, long long slot_stride, int num_pages, int page_size,

@@ -662,6 +662,7 @@ int entmax_attn_page_tables(const int32_t* lens, const int32_t* new_lens,
   if (!lens || !new_lens || (!free_pages && n_free != 0) || !free_start || !block_tables ||
       (!slots) != (n_new == 0) || !lens_out || !cu_new || !free_next || n_free < 0 || W < 1 ||
       B < 1 || B > ea::kMaxRequests || table_stride < W || page_size < 1 || n_new < 0 ||
+      n_new > 0x7fffffff - 4 ||  // slots are numbered four at a time in 32 bits
       (padded != 0 && padded != 1) || lens_out == lens || lens_out == new_lens ||
       free_next == free_start || static_cast<int64_t>(B) * W >= (int64_t(1) << 31))
     return ENTMAX_ATTN_EINVAL;

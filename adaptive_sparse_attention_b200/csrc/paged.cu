@@ -30,18 +30,27 @@ __device__ __forceinline__ Grow grow_of(const PageTables& P, int b) {
   return r;
 }
 
-// Block-wide inclusive scans of two values at once; totals in tx, ty.
+// Sums of new tokens stop at 2^31 - 1, so that the prefix sums never fall: no lengths send a search
+// or an index outside.  (The pages add up to less than 2^31, see the host checks.)
+__device__ __forceinline__ int add_tokens(int a, int b) {  // both >= 0
+  return static_cast<int>(min(static_cast<unsigned>(a) + static_cast<unsigned>(b), 0x7fffffffu));
+}
+
+// Block-wide exclusive scans of two values at once, x by add_tokens; totals in tx, ty.
 __device__ __forceinline__ void scan2(int& x, int& y, int2* buf, int& tx, int& ty) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int a = __shfl_up_sync(kFull, x, o), b = __shfl_up_sync(kFull, y, o);
     if (lane >= o) {
-      x += a;
+      x = add_tokens(x, a);
       y += b;
     }
   }
   if (lane == 31) buf[warp] = make_int2(x, y);
+  x = __shfl_up_sync(kFull, x, 1);
+  y = __shfl_up_sync(kFull, y, 1);
+  if (lane == 0) x = y = 0;
   __syncthreads();
   int bx = 0, by = 0;
   tx = ty = 0;
@@ -49,13 +58,13 @@ __device__ __forceinline__ void scan2(int& x, int& y, int2* buf, int& tx, int& t
   for (int w = 0; w < kTableWarps; ++w) {
     const int2 v = buf[w];
     if (w < warp) {
-      bx += v.x;
+      bx = add_tokens(bx, v.x);
       by += v.y;
     }
-    tx += v.x;
+    tx = add_tokens(tx, v.x);
     ty += v.y;
   }
-  x += bx;
+  x = add_tokens(x, bx);
   y += by;
 }
 
@@ -98,20 +107,19 @@ __global__ void __launch_bounds__(kTableThreads) page_tables_kernel(const PageTa
     int toks = 0, pages = 0;
     for (int b = b0; b < b1; ++b) {
       const Grow r = grow_of(P, b);
-      toks += r.add;
+      toks = add_tokens(toks, r.add);
       pages += r.need - r.have;
     }
     int x = toks, y = pages, tx, ty;
     scan2(x, y, buf, tx, ty);
-    x -= toks;
-    y -= pages;
     for (int b = b0; b < b1; ++b) {
       const Grow r = grow_of(P, b);
-      const int x1 = x + r.add, y1 = y + r.need - r.have;
+      const int x1 = add_tokens(x, r.add), y1 = y + r.need - r.have;
       // A request is served if its lengths fit, its tokens lie inside the slots and its pages
       // inside the free list.  Requests that take pages are served in order until the list is
       // exhausted.
-      const bool ok = r.ok && (P.padded || x1 <= P.n_new) && (r.need == r.have || y1 <= avail);
+      const bool ok = r.ok && x1 < 0x7fffffff && (P.padded || x1 <= P.n_new) &&
+                      (r.need == r.have || y1 <= avail);
       req[b] = {x, y, ok ? P.lens[b] : -1, r.have};
       x = x1;
       y = y1;

@@ -290,17 +290,19 @@ int entmax_attn_route_chunks(const void* q, const void* summaries, float* pi, fl
  *           start at cu_new[b]), -1 behind the last; padded = 1: int64 [B][n_new], token t of
  *           request b at [b][t], -1 for t >= new_lens[b].  NULL with n_new = 0: a step without
  *           tokens.
- *   lens_out int32 [B]: the lengths after the step.  cu_new int32 [B + 1]: prefix sums of new_lens.
+ *   lens_out int32 [B]: the lengths after the step.  cu_new int32 [B + 1]: prefix sums of new_lens
+ *           (a negative one counts as 0), which stop at 2^31 - 1.
  *   free_next int32 [1]: free_start after the step.
  * A request that does not fit keeps its length, takes no page, and its tokens get slot -1: one
- * whose lengths are negative or exceed W * page_size tokens, whose tokens lie beyond the slots, or
- * whose pages lie beyond entry n_free (requests are served in order; once one runs out of pages,
- * so does every later one that needs a page).  A token whose page is a table entry below 0 gets
- * slot -1.  The sums of new_lens and B * W must stay below 2^31.
+ * whose lengths are negative or exceed W * page_size tokens, whose tokens lie beyond the slots or
+ * where cu_new has stopped, or whose pages lie beyond entry n_free (requests are served in order;
+ * once one runs out of pages, so does every later one that needs a page).  A token whose page is a
+ * table entry below 0 gets slot -1.  No lengths, table entries or free pages make the call read or write outside its arrays.
  * Outputs may not overlap inputs (block_tables is both).  Device pointers, aligned to their
  * element size; asynchronous on `stream`.  Returns ENTMAX_ATTN_OK, ENTMAX_ATTN_EINVAL (null pointer,
- * size < 1 except n_new = 0 with slots NULL, n_free < 0, B > 8192, table_stride < W, padded not 0/1, lens_out == lens or new_lens,
- * free_next == free_start), ENTMAX_ATTN_EALIGN or ENTMAX_ATTN_ECUDA. */
+ * size < 1 except n_new = 0 with slots NULL, n_new > 2^31 - 5, n_free < 0, B > 8192, B * W >= 2^31,
+ * table_stride < W, padded not 0/1, lens_out == lens or new_lens, free_next == free_start),
+ * ENTMAX_ATTN_EALIGN or ENTMAX_ATTN_ECUDA. */
 int entmax_attn_page_tables(const int32_t* lens, const int32_t* new_lens,
                             const int32_t* free_pages, int n_free, const int32_t* free_start,
                             int32_t* block_tables, long long table_stride, int W, int B,

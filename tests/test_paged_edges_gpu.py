@@ -97,3 +97,28 @@ def test_sizes_that_are_wrong_are_still_refused():
         ea.alloc_decode_workspace(q, kc, -1)
     with pytest.raises((ValueError, _native.EntmaxAttnError)):
         ea.page_tables(lens, lens, lens, lens[:1], tables, 16, -1)
+
+
+@pytest.mark.parametrize("padded", [False, True])
+@pytest.mark.parametrize("B", [4, 600])
+def test_tables_with_token_counts_that_add_up_past_2_31(B, padded):
+    """Huge counts do not fit their table rows; cu_new stops at 2^31 - 1, and no request behind that
+    is served (packed), none with a huge count either way."""
+    big = (1 << 31) - 1
+    new = np.tile([3, big, 7, 5], B // 4)
+    if padded:
+        new[2] = big
+    lens = np.tile([0, 2, 30, 1], B // 4)
+    tables = i32(np.full((B, 5), -1))
+    free = list(range(4 * B))
+    at = np.minimum(np.concatenate([[0], np.cumsum(new)]), big)
+    got = ea.page_tables(i32(lens), i32(new), i32(free), i32([0]), tables, 16, 20, padded)
+    assert np.array_equal(got[2].cpu().numpy(), at)
+    serve = (new < big) & (at[1:] < big) & (padded | (at[1:] <= 20))
+    assert serve.any()
+    assert np.array_equal(got[1].cpu().numpy(), np.where(serve, lens + new, lens))
+    slots = got[0].cpu().numpy()
+    assert (slots >= 0).sum() == new[serve].sum()
+    assert np.all((tables.cpu().numpy() >= 0).any(1) <= serve)
+    if not padded:
+        assert (slots[:3] >= 0).all() and (slots[3:] == -1).all()

@@ -43,8 +43,9 @@ def _on(stream, dev):
     if isinstance(stream, torch.cuda.Stream) and stream.device != dev:
         raise ValueError(f"the stream is on {stream.device}, the tensors are on {dev}")
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(
-            stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream), dev)
+        raw = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+        # torch takes an external handle of 0 for none given and makes a new stream
+        stream = torch.cuda.ExternalStream(raw, dev) if raw else torch.cuda.default_stream(dev)
     return torch.cuda.stream(stream)
 
 
@@ -59,9 +60,10 @@ def page_tables(lens, new_lens, free_pages, free_start, block_tables, page_size:
     cu_new, free_next): slots int64 [n_new], the new tokens packed in request order and -1 behind
     the last, or with padded=True [B, n_new], -1 for t >= new_lens[b]; lens_out int32 [B]; cu_new
     int32 [B + 1], the prefix sums of new_lens (the cu_seqlens of the packed forward pass); free_next
-    int32 [1].  B is at least 1; n_new may be 0.  A request that does not fit keeps its length and gets slots of -1 (see
-    include/entmax_attn.h).  The outputs may be given; lens_out and free_next may not be the
-    inputs themselves.  Where none of lens_out, cu_new and free_next is, they share one storage."""
+    int32 [1].  B is at least 1; n_new may be 0.  A request that does not fit keeps its length and
+    gets slots of -1 (see include/entmax_attn.h).  The outputs may be given; lens_out and free_next
+    may not be the inputs themselves.  Where none of lens_out, cu_new and free_next is, they share
+    one storage."""
     if stream is not None:
         with _on(stream, lens.device):
             return page_tables(lens, new_lens, free_pages, free_start, block_tables, page_size,

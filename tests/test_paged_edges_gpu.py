@@ -122,3 +122,31 @@ def test_tables_with_token_counts_that_add_up_past_2_31(B, padded):
     assert np.all((tables.cpu().numpy() >= 0).any(1) <= serve)
     if not padded:
         assert (slots[:3] >= 0).all() and (slots[3:] == -1).all()
+
+
+@pytest.mark.parametrize("raw", [False, True])
+def test_the_default_stream_by_its_handle(raw):
+    """Handle 0 is the default stream, also while another one is current: the calls see what was
+    queued there before them, and what is queued there next sees their results."""
+    q, kc, vc, tables, lens = unused_batch(2, 4, 2, 64, "bf16")
+    default = torch.cuda.default_stream()
+    assert default.cuda_stream == 0
+    stream = 0 if raw else default
+    k = torch.randn(2, 5, 64).bfloat16().cuda()
+    new, free, start, table = i32([3, 2]), i32([3, 2, 1]), i32([0]), i32([[0, -1, -1], [1, -1, -1]])
+    torch.cuda.synchronize()
+    with torch.cuda.stream(torch.cuda.Stream()):
+        with torch.cuda.stream(default):
+            torch.cuda._sleep(20_000_000)  # about 10 ms
+            tables.copy_(table)
+            lens.fill_(1)
+        slots, n, _, _ = ea.page_tables(lens, new, free, start, tables, 16, 5, stream=stream)
+        ea.paged_append(k, k, kc, vc, slots, stream=stream)
+        out, tau = ea.entmax_attn_decode(q, kc, vc, tables, n, 1.5, stream=stream)
+        with torch.cuda.stream(default):
+            seen = [x.clone() for x in (n, slots, kc, tau)]
+    torch.cuda.synchronize()
+    assert seen[0].tolist() == [4, 3]
+    assert seen[1].tolist() == [1, 2, 3, 17, 18]
+    assert torch.equal(seen[2][0, :, 1:4], k[:, :3]) and torch.equal(seen[2][1, :, 1:3], k[:, 3:])
+    assert torch.isfinite(seen[3]).all()

@@ -28,7 +28,6 @@
 
 #include <cuda_bf16.h>
 
-#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -1176,20 +1175,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps) decode_join_many_kernel(const
     }
   }
   join_many<T, D, BK, true>(P, sm, valid, head);
-}
-
-// Allows a kernel more than 48 KB of shared memory, once per device.
-template <typename K>
-cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done) {
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
-  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           static_cast<int>(bytes));
-  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
 }
 
 template <typename T, int D, int NT>

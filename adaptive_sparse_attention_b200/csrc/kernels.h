@@ -3,6 +3,7 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cmath>
 
 #include "common.cuh"
@@ -88,6 +89,21 @@ __device__ __forceinline__ void serial_wait() {
   asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 #endif
+// Allows a kernel more than 48 KB of shared memory, once per device and always the most that any of
+// its launches takes: the limit is the process's, and another thread may be about to launch with it.
+template <typename K>
+cudaError_t allow_smem(K kern, size_t bytes, std::atomic<uint64_t>& done) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           static_cast<int>(bytes));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 constexpr int kMaxRequests = 8192;  // prefix sums over the batch live in shared memory
 
 // Block tables and slot maps of a step (entmax_attn_page_tables).

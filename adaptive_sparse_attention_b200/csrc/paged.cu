@@ -247,8 +247,9 @@ cudaError_t launch_page_tables(const PageTables& P, cudaStream_t s) {
   const int grid = static_cast<int>(want < 1 ? 1 : want > 148 ? 148 : want);
   const size_t smem = sizeof(Entry) * (P.B + 1);
   if (smem > 48 * 1024) {
-    const cudaError_t e = cudaFuncSetAttribute(
-        page_tables_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e =
+        allow_smem(page_tables_kernel, sizeof(Entry) * (kMaxRequests + 1), done);
     if (e != cudaSuccess) return e;
   }
   return launch_serial(page_tables_kernel, dim3(grid), dim3(kTableThreads), smem, s, 1, P);

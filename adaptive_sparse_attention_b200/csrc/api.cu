@@ -15,8 +15,11 @@
 #include "entmax_attn.h"
 #include "kernels.h"
 
-// Per-device status word: kernels set ENTMAX_ATTN_ETIMEOUT here when a bounded wait gives up.
-__device__ int g_entmax_status;
+// Per-device status words: kernels set the first to ENTMAX_ATTN_ETIMEOUT when a bounded wait gives
+// up, the second (kRangeWord) to ENTMAX_ATTN_ERANGE when a length, page or slot is out of range, so
+// that neither hides the other.
+__device__ int g_entmax_status[2];
+constexpr int kRangeWord = 1;
 
 namespace {
 
@@ -716,6 +719,7 @@ int entmax_attn_paged_append(const void* k, const void* v, long long stride_b, l
   int err = ENTMAX_ATTN_OK;
   P.status = status_ptr(&err);
   if (!P.status) return err;
+  P.status += kRangeWord;
   P.k = k;
   P.v = v;
   P.k_cache = k_cache;
@@ -775,6 +779,7 @@ int entmax_attn_decode(const void* q, long long q_stride_b, long long q_stride_h
   int err = ENTMAX_ATTN_OK;
   P.status = status_ptr(&err);
   if (!P.status) return err;
+  P.status += kRangeWord;
   P.q = q;
   P.k = k_cache;
   P.v = v_cache;
@@ -838,13 +843,14 @@ int entmax_attn_fallback_tiles(const void* workspace, cudaStream_t stream) {
 int entmax_attn_status(cudaStream_t stream) {
   cudaError_t e = cudaStreamSynchronize(stream);
   if (e != cudaSuccess) return cuda_fail(e);
-  int v = 0;
-  e = cudaMemcpyFromSymbol(&v, g_entmax_status, sizeof(int));
+  int v[2] = {0, 0};
+  e = cudaMemcpyFromSymbol(v, g_entmax_status, sizeof(v));
   if (e != cudaSuccess) return cuda_fail(e);
+  const int w = v[0] != ENTMAX_ATTN_OK ? 0 : kRangeWord;
   const int zero = 0;
-  e = cudaMemcpyToSymbol(g_entmax_status, &zero, sizeof(int));
+  e = cudaMemcpyToSymbol(g_entmax_status, &zero, sizeof(int), w * sizeof(int));
   if (e != cudaSuccess) return cuda_fail(e);
-  return v;
+  return v[w];
 }
 
 void entmax_attn_release_workspaces(void) {

@@ -364,7 +364,8 @@ int entmax_attn_decode(const void* q, long long q_stride_b, long long q_stride_h
                        float alpha, int n_iter, int dtype, cudaStream_t stream);
 
 /* Synchronises `stream`, returns the device status word of the current device
- * (ENTMAX_ATTN_OK, ENTMAX_ATTN_ETIMEOUT or ENTMAX_ATTN_ERANGE) and clears it. */
+ * (ENTMAX_ATTN_OK, ENTMAX_ATTN_ETIMEOUT or ENTMAX_ATTN_ERANGE) and clears it.  With both latched it
+ * reports and clears ENTMAX_ATTN_ETIMEOUT, and the next call ENTMAX_ATTN_ERANGE. */
 int entmax_attn_status(cudaStream_t stream);
 
 /* Frees the workspaces entmax_attn_fwd cached (synchronises the device first). */

@@ -84,6 +84,14 @@ at::Tensor output(PyObject* o, const char* name, at::IntArrayRef shape, at::Scal
   return t;
 }
 
+// Whether two tensors of one shape are laid out alike: a dimension of one element may carry any
+// stride.
+bool same_layout(const at::Tensor& a, const at::Tensor& b) {
+  for (int64_t i = 0; i < a.dim(); ++i)
+    if (a.size(i) > 1 && a.stride(i) != b.stride(i)) return false;
+  return true;
+}
+
 struct Cache {
   const at::Tensor& k;
   const at::Tensor& v;
@@ -98,7 +106,7 @@ Cache cache(PyObject* ko, PyObject* vo) {
       (k.scalar_type() != at::kFloat && k.scalar_type() != at::kBFloat16))
     refuse("k_cache must be a float32 or bfloat16 CUDA tensor [num_pages, Hkv, page_size, d] with "
            "a unit-stride last dimension");
-  if (v.sizes() != k.sizes() || v.strides() != k.strides() || v.scalar_type() != k.scalar_type() ||
+  if (v.sizes() != k.sizes() || !same_layout(k, v) || v.scalar_type() != k.scalar_type() ||
       v.device() != k.device())
     refuse("v_cache must have the shape, strides, dtype and device of k_cache");
   for (int i = 0; i < 4; ++i)
@@ -200,7 +208,7 @@ PyObject* paged_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
     if (H != c.heads || k.size(dim - 1) != c.d || k.scalar_type() != c.k.scalar_type() ||
         k.device() != c.dev || k.stride(dim - 1) != 1)
       refuse("k must have the cache's heads, head size, dtype and device, and unit-stride rows");
-    if (v.sizes() != k.sizes() || v.strides() != k.strides() ||
+    if (v.sizes() != k.sizes() || !same_layout(k, v) ||
         v.scalar_type() != k.scalar_type() || v.device() != c.dev)
       refuse("v must have the shape, strides, dtype and device of k");
     if (slots.scalar_type() != at::kLong || slots.device() != c.dev || !slots.is_contiguous() ||

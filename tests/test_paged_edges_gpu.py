@@ -150,3 +150,33 @@ def test_the_default_stream_by_its_handle(raw):
     assert seen[1].tolist() == [1, 2, 3, 17, 18]
     assert torch.equal(seen[2][0, :, 1:4], k[:, :3]) and torch.equal(seen[2][1, :, 1:3], k[:, 3:])
     assert torch.isfinite(seen[3]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_strides_of_dimensions_of_one_element_do_not_matter(dtype):
+    """k from a projection of its own, v a slice of a fused one: they differ only in the strides of
+    the batch, head or token dimension of one element; so do caches of one page or head."""
+    d, P = 64, 4
+    fused = torch.randn(1, 1, 3 * d).to(DT[dtype]).cuda()
+    v = fused[..., 2 * d:].view(1, 1, 1, d)
+    k = torch.randn(1, 1, 1, d).to(DT[dtype]).cuda().as_strided((1, 1, 1, d), (8 * d, 1, 7, 1))
+    assert k.stride() != v.stride()
+    kc = torch.zeros(1, 1, P, d, dtype=DT[dtype], device="cuda")
+    vc = torch.zeros(1, P, 1, d, dtype=DT[dtype], device="cuda").transpose(1, 2).as_strided(
+        (1, 1, P, d), (3, 5, d, 1))
+    assert kc.stride() != vc.stride()
+    slots = torch.tensor([2], device="cuda")
+    ea.paged_append(k, v, kc, vc, slots)
+    assert torch.equal(kc[0, 0, 2], k[0, 0, 0]) and torch.equal(vc[0, 0, 2], v[0, 0, 0])
+    ea.paged_append(k[0], v[0], kc, vc, slots)
+    q = torch.randn(1, 2, d).to(DT[dtype]).cuda()
+    vc[0, 0, 0] = 1.0
+    a = ea.entmax_attn_decode(q, kc, vc, i32([[0]]), i32([3]))
+    b = ea.entmax_attn_decode(q, kc, vc.clone(memory_format=torch.contiguous_format), i32([[0]]),
+                              i32([3]))
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    with pytest.raises(ValueError):  # a difference that matters
+        two = torch.zeros(2, 1, P, d, dtype=DT[dtype], device="cuda")
+        ea.entmax_attn_decode(q, two, two.expand(2, 1, P, d).as_strided((2, 1, P, d),
+                                                                       (d, P * d, d, 1)),
+                              i32([[0]]), i32([3]))

@@ -22,6 +22,8 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libentmax_attn.so")
 BINDING = os.path.join(PKG, "_paged.so")
+BINDING_SOURCE = os.path.join(CSRC, "paged_binding.cpp")
+BINDING_STAMP = os.path.join(BUILD, "paged_binding.txt")  # what BINDING was compiled against
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-Wall",
@@ -83,13 +85,29 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
     return LIB
 
 
+def _binding_abi() -> str:
+    import torch
+    return f"torch {torch.__version__}, {sys.implementation.cache_tag}\n"
+
+
+def binding_stale() -> bool:
+    """Whether _paged.so is older than its sources or was compiled against another torch or Python,
+    whose C++ interfaces differ."""
+    try:
+        with open(BINDING_STAMP) as f:
+            stamp = f.read()
+    except OSError:
+        return True
+    return stamp != _binding_abi() or _stale(BINDING, [BINDING_SOURCE] + headers() + [__file__])
+
+
 def build_binding(force: bool = False, verbose: bool = False) -> str:
     """_paged.so: csrc/paged_binding.cpp over torch's C++ tensors, linked to libentmax_attn.so."""
-    src = os.path.join(CSRC, "paged_binding.cpp")
-    if force or _stale(BINDING, [src] + headers() + [__file__]):
+    if force or binding_stale():
         import sysconfig
 
         import torch
+        os.makedirs(BUILD, exist_ok=True)
         root = os.path.dirname(torch.__file__)
         cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
         inc = [os.path.join(root, "include"),
@@ -99,7 +117,7 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall"]
         for d in inc:
             cmd += ["-isystem" if d != INCLUDE else "-I", d]
-        cmd += [src, "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
+        cmd += [BINDING_SOURCE, "-o", tmp, "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu",
                 "-ltorch_cuda", "-ltorch", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:" + os.path.basename(LIB),
                 "-Wl,-rpath,$ORIGIN"]
         r = subprocess.run(cmd, capture_output=True, text=True)
@@ -108,6 +126,8 @@ def build_binding(force: bool = False, verbose: bool = False) -> str:
         if r.returncode != 0:
             raise RuntimeError("building the paged-cache binding failed")
         os.replace(tmp, BINDING)
+        with open(BINDING_STAMP, "w") as f:
+            f.write(_binding_abi())
     return BINDING
 
 

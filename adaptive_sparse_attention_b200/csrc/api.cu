@@ -521,22 +521,34 @@ size_t decode_layout(void* base, int B, int Hq, int Hkv, int max_len, ea::Decode
   return off;
 }
 
-// Which of the decode kernels serves a call, from its sizes alone (the lengths are on the device).
-// Times on a B200 in us of a captured call, bf16, d = 128, Hkv = 8, G = 4, alpha = 1.5 with key
-// spikes, all lengths equal unless said otherwise.
+// Which of the decode kernels serves a call, from its sizes and max_len alone (the lengths are on the
+// device).  Times on a B200 in us per call, in a graph of calls on different caches (600 MB in all, so
+// that none is in L2), bf16, d = 128, Hkv = 8, G = 4, alpha = 1.5 with key spikes, every length equal
+// to max_len, unless said otherwise; "against": the split kernels with the join that they would have.
 //   cluster: C = 8, 4, 2 or 1 blocks per (request, head group), the most that run all at once (2
-//     blocks per SM).  One launch and no prefix sums, about 2 us ahead of the split kernels, more
-//     for batches (B = 1, 1000 keys: 10.4 against 12.4; B = 16, 128 keys: 14.5 against 16.6, 4096
-//     keys: 31 against 33; B = 33, d = 64, G = 1, lengths to 4096: 25 against 33), but a block
-//     reads about 44 GB/s, so a request much longer than the others, or alone, is late: 1 request
-//     of 16384 keys takes 17.4 against 16.6, of 131072 98 against 53.  So they serve a single
-//     request as long as its blocks' extra time against the 6.3 TB/s of the split kernels is below
-//     those 2 us, and a batch if its longest possible request is read in 12 us.
-//   join_blocks of the split kernels: up to 148 heads have a cluster of 4 blocks each (B = 4,
-//     lengths to 20000, alpha = 1.333 without spikes: 37 against 41 with one block; 2 us more with
-//     few candidates), up to 1024 a block each (B = 16, 4096 keys: 33 against 35 with a warp each),
-//     more a warp each (B = 64, 128 keys: 18.6 against 33 with a block each, 16384 keys 342 against
-//     353).
+//     blocks per SM; for batches of short requests fewer would do: 16 of 128 keys 13.6, with C = 1
+//     10.3).  One launch and no prefix sums: 1 request of 1000 keys takes 8.9 against 11.7, 4 of 8192
+//     19.6 against 25.8, 16 of 4096 31.4 against 35.8.  But a block reads about 44 GB/s, so a request
+//     much longer than the others, or alone, is late.
+//     Single requests: the extra time of its blocks over the 6.3 TB/s of the split kernels may be 4
+//     us.  5000 keys (2.0 us of it) take 11.5 against 14.5, 8192 (3.3) 13.8 against 15.2, 12434 (5.0)
+//     17.2 against 17.6, 16384 (6.6) 19.6 against 18.3, 131072 98 against 55; one kv head of 8 query
+//     heads, 4096 keys (2.8) 10.2 against 10.6, 8192 (5.6) 12.9 against 12.0; fp32, 4096 keys (3.3)
+//     14.6 against 15.6, 8192 (6.6) 21.2 against 19.0; d = 64, G = 1, 16384 keys (3.3) 16.1 against
+//     15.5.
+//     Batches: the longest possible request may take its blocks 12 us.  Up to there the cluster kernel
+//     is ahead or level for full and for ragged batches; from there to 24 us it depends on lengths
+//     and candidates, which are not known here.  14.5 us: 4 requests of 20000 keys 35.2 against 40.2,
+//     but with lengths spread evenly, alpha = 1.333 and no spikes 46.2 against 42.9.  24 us: 4 of
+//     32768 51.4 against 56.4, 33 of 4096 53.9 against 60.3, but 16 of 1 to 8192 40.3 against 37.1,
+//     and 33 of 0 to 8192, d = 64, G = 1, 47.7 against 35.1.
+//     max_len is what a caller allows, not what the requests hold: with max_len = 131072 a single
+//     request of 1000 keys takes 11.6, with max_len = 1000 8.9.
+//   join_blocks of the split kernels: up to 148 heads have a cluster of 4 blocks each (4 requests of up
+//     to 20000, alpha = 1.333 without spikes, 43.0 against 45.0 with one block; about 1.5 us more
+//     with few candidates), up to 1024 a block each (16 of 4096: 35.8 against 37.4 with a warp
+//     each), more a warp each (33 of 1024: 29.0 against 30.4 with a block each; 33 of 4096: 61.2
+//     against 64.7).
 void choose_decode_kernels(ea::DecodeProblem* P, double row_bytes) {
   const int64_t groups = static_cast<int64_t>(P->B) * P->Hkv * P->head_blocks;
   P->cluster = 0;
@@ -545,7 +557,7 @@ void choose_decode_kernels(ea::DecodeProblem* P, double row_bytes) {
     while (groups * c > 2 * 148) c /= 2;
     const double bytes = P->max_len * row_bytes;  // of the longest request and one kv head
     const double block_us = bytes / (c * 44e3);
-    if (P->B == 1 ? block_us - groups * bytes / 6300e3 <= 2.0 : block_us <= 12.0) P->cluster = c;
+    if (P->B == 1 ? block_us - groups * bytes / 6300e3 <= 4.0 : block_us <= 14.0) P->cluster = c;
   }
   const int64_t heads = static_cast<int64_t>(P->B) * P->Hq;
   P->join_blocks = heads <= 148 ? 4 : heads <= 1024 ? 1 : 0;

@@ -495,6 +495,7 @@ struct JoinSmem {
   float2 all[W > 1 ? kSolo : 1];  // all candidates, when they are few
   Row rows[W][32];
   float2 sums[2][C * W];
+  float2 bound;  // m and the bound of t, one pair for the whole join
   float red[W];
   int count[C * W];
   float co[C > 1 ? C : 1][C > 1 ? 128 : 1];  // the blocks' sums of o
@@ -563,21 +564,21 @@ __device__ __forceinline__ void warp_sum2(float& a, float& b) {
 struct Parts {
   const int2* info;      // (count, max bits) of each
   int np;                // number of parts
+  int most;              // no more than this, whatever the workspace holds
   int run, off, nb;      // part i starts at unit i run - off of the nb units of the request
   __device__ __forceinline__ int2 part(int i) const { return info[i]; }
   __device__ __forceinline__ int key0(int i) const { return min(max(i * run - off, 0), nb) * 16; }
 };
 
 // From the maxima of a head's parts: its largest score m, and a lower bound of t = tau - m.  The
-// maxima
-// are scores of the head, and the tau of a part of the keys is at most that of all (more keys only
-// add to the sum), so a few of the steps above on up to 256 of them give a bound far above -1:
+// maxima are scores of the head, and the tau of a part of the keys is at most that of all (more keys
+// only add to the sum), so a few of the steps above on up to 256 of them give a bound far above -1:
 // of 20000 normal scores at alpha = 1.333, 184 lie above tau, 226 above the bound from 64 maxima
 // and 3496 above m - 1.  Where at most half of the parts reach above m - 1 the candidates are few
 // and the bound is -1.  (The parts' counts do not enter: in the cluster kernel they depend on
 // the timing, and the bound decides in which order the sums below add.)  Every warp computes both,
-// so that they need no barrier; red: for more than 256 parts, whose maximum the block takes
-// together.
+// so that they need no barrier; red: where there may be more than 256 parts, whose maximum the block
+// takes together.
 struct Bounds {
   float m, floor;  // floor: of t
 };
@@ -600,7 +601,7 @@ __device__ __forceinline__ Bounds part_bounds(const DecodeProblem& P, float* red
       r.m = max_nan(r.m, __int_as_float(parts.part(i).y));
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) r.m = max_nan(r.m, __shfl_xor_sync(kFull, r.m, o));
-  if (W > 1 && np > 32 * R) {
+  if (W > 1 && parts.most > 32 * R) {
     if (lane == 0) red[threadIdx.x >> 5] = r.m;
     __syncthreads();
     r.m = red[lane % W];
@@ -641,7 +642,7 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
   constexpr int kList = JoinSmem<W, C>::kList;
   const int lane = threadIdx.x & 31, warp = W == 1 ? 0 : threadIdx.x >> 5;
   const int me = rank * W + warp;
-  const float m = bound.m, floor = bound.floor;
+  float m = bound.m, floor = bound.floor;
   const int tid = W == 1 ? lane : threadIdx.x;
   const int hk = h / P.G;
   const int64_t row = static_cast<int64_t>(b) * P.Hq + h;
@@ -652,11 +653,11 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
       if (tid == 0) P.tau[row] = NAN;
     }
   };
-  if (!(m > -INFINITY)) return undefined();  // a NaN, or every score -inf: p is not defined
 
   // Each warp compacts the entries above the bound of a contiguous range of parts, in order and as
-  // (z - m, key): the first kList into shared memory, the others back to the front of the range (an entry only moves
-  // forward, over places that the warp has read already, since it reads them in order).
+  // (z - m, key): the first kList into shared memory, the others back to the front of the range (an
+  // entry only moves forward, over places that the warp has read already, since it reads them in
+  // order).
   int2* cand = P.cand + row * P.cand_stride;
   const int i_end = (me + 1) * np / kAll;
   const int i_beg = me * np / kAll;
@@ -715,10 +716,19 @@ __device__ __forceinline__ void join_head(const DecodeProblem& P, JoinSmem<W, C>
   // When the candidates are few, the first warp takes them all and finds tau and the p by itself,
   // with no sum over the warps or blocks per step, and deals the values to add to its block's
   // warps.
+  // All blocks and warps go by one m and bound, so that each takes the same barriers and no block
+  // leaves while another stores into its shared memory, whatever another call that was given the same
+  // workspace wrote in between.
   bool solo = W == 1;
   if (W > 1) {
     share<C>(&sm.count[me], n_list);
+    if (me == 0) share<C>(&sm.bound, make_float2(m, floor));
     join_sync<W, C>();
+    m = sm.bound.x;
+    floor = sm.bound.y;
+  }
+  if (!(m > -INFINITY)) return undefined();  // a NaN, or every score -inf: p is not defined
+  if (W > 1) {
     // inclusive scan of the counts, lane l holding those of warps K l .. K l + K - 1
     constexpr int K = kAll > 32 ? kAll / 32 : 1;
     int x = 0;
@@ -1054,8 +1064,10 @@ __device__ __forceinline__ Parts split_parts(const DecodeProblem& P, int b, int 
   const int HG = P.Hkv * P.head_blocks, hg = hk * P.head_blocks + hb;
   Parts r;
   r.nb = (len + 15) >> 4;
-  // What is read from the workspace is clamped throughout the join, so that one that another call
-  // overwrites meanwhile spoils the results but sends no access outside.
+  r.most = r.nb;
+  // What is read from the workspace is clamped throughout the join and decides about no barrier (see
+  // join_head), so that one that another call overwrites meanwhile spoils the results but sends no
+  // access outside and leaves no block waiting.
   const int units = min(max(P.pre[P.B], r.nb), static_cast<int>(P.B * (P.cand_stride >> 4)));
   r.run = (units * HG + P.score_warps - 1) / P.score_warps;
   const int A = min(max(P.pre[b], 0), units - r.nb) * HG + hg * r.nb;  // the group's first unit
@@ -1230,7 +1242,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps, 2) decode_cluster_kernel(cons
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   const int raw_len = P.lens[b], len = clamped_len(P, b);
   Parts parts;
-  parts.np = blocks * kJoinWarps;
+  parts.np = parts.most = blocks * kJoinWarps;
   parts.nb = (len + 15) >> 4;
   parts.run = (parts.nb + parts.np - 1) / parts.np;
   parts.off = 0;

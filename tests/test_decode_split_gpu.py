@@ -190,3 +190,26 @@ def test_split_on_two_streams_and_in_a_graph(alpha, oracle):
     for x, got, ref in zip(c, outs, want):
         assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])
         x.check(*got, alpha)
+
+
+@pytest.mark.parametrize("join", JOINS)
+def test_split_calls_that_share_a_workspace_end(join):
+    """Calls that overlap need a workspace each; with one between them their results are undefined, but
+    what they read of it reaches no index beyond their buffers and no barrier, so that both end and
+    later calls are right."""
+    n = repeats(join, 4 * 8)
+    c = [case(lens * n, 8, 2, 64, 16, "bf16", seed=s, spikes=0.0)
+         for s, lens in ((20, [6000, 100, 0, 900]), (21, [1, 4000, 9000, 16]))]
+    want = [split_run(x, 1.333) for x in c]
+    ws = ea.alloc_decode_workspace(c[0].q, c[0].kc, LIMIT)
+    streams = [torch.cuda.Stream() for _ in c]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for x, s in zip(c, streams):
+            ea.entmax_attn_decode(x.q, x.kc, x.vc, x.d_tables, x.d_lens, 1.333, max_len=LIMIT,
+                                  workspace=ws, stream=s)
+    torch.cuda.synchronize()
+    assert ea.status() == 0
+    for x, ref in zip(c, want):
+        got = split_run(x, 1.333)
+        assert torch.equal(got[0], ref[0]) and torch.equal(got[1], ref[1])

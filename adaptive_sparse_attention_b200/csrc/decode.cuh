@@ -5,7 +5,9 @@
 //   o = sum_j p_j v_j
 // with key j in slot j % page_size of page block_tables[b][j / page_size].
 //
-// Two steps.  The scores: every key is read once, and per (request, head) the keys that can carry
+// Two steps.  The scores: every key is read once (for each 16 query heads of its kv head; the form for
+// more than 8 spills registers, and one request of 32768 keys and 8 kv heads takes 34.9 us with 16
+// query heads each, 24.3 with 8), and per (request, head) the keys that can carry
 // p > 0 are kept (z > max - 1, since p <= 1 gives tau >= max - 1).  The join: the max m over all
 // parts, tau, and o from the values of the keys with z > tau.  A softmax would have to read every
 // value too; here the values of keys with p = 0 are never read, so the traffic is that of the keys
@@ -1222,7 +1224,7 @@ cudaError_t launch_join(const DecodeProblem& P, cudaStream_t s) {
 // A cluster of P.cluster (1 to 8) blocks scores one (request, head group), each of its warps an
 // equal run of units, and after a cluster barrier its blocks join the group's heads.  One launch
 // and no prefix sums: less latency than the split kernels, as long as all clusters run at once.
-// One request of 1000 tokens takes 8.8 us, 4 of 16384 29 us (4.6 TB/s); a block alone on its SM
+// One request of 1000 tokens takes 8.6 us, 4 of 16384 30 us (4.4 TB/s); a block alone on its SM
 // reads 44 GB/s, 64 KB in flight over a latency of 1.4 us.
 constexpr int kClusterBlocks = 8;  // at most
 template <typename T, int D, int NT, int BK>

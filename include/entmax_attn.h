@@ -326,12 +326,14 @@ int entmax_attn_paged_append(const void* k, const void* v, long long stride_b, l
                              int num_pages, int page_size, const int64_t* slots, int B, int Hkv,
                              int T, int d, int dtype, cudaStream_t stream);
 
-/* Bytes of workspace entmax_attn_decode needs for requests of up to max_len tokens; 0 on bad
- * sizes and for max_len = 0. */
+/* Bytes of workspace entmax_attn_decode needs for requests of up to max_len tokens, 0 on bad sizes
+ * and for max_len = 0: about 8 * B * Hq * max_len, a place for every score, whatever the lengths. */
 size_t entmax_attn_decode_workspace_bytes(int B, int Hq, int Hkv, int max_len);
 
 /* alpha-entmax attention of one new token per request over its paged keys and values: the forward
- * pass for q of one row per (request, head), which sees all seq_lens[b] keys.
+ * pass for q of one row per (request, head), which sees all seq_lens[b] keys.  The keys of a kv head
+ * are read once for each 16 of its query heads.  Which kernels run follows from the sizes and max_len,
+ * not from the lengths: a max_len near them is faster.
  *   q: element e of (b, h) at b * q_stride_b + h * q_stride_h + e (strides in elements, multiples of
  *      16 bytes); out [B, Hq, d] contiguous, q's dtype; tau fp32 [B, Hq].
  *   seq_lens int32 [B], at most max_len <= W * page_size.  max_len = 0, for a batch of unused rows,

@@ -11,7 +11,7 @@ pytestmark = pytest.mark.gpu
 
 
 def test_page_tables_of_different_batches_at_once():
-    """Batches from 3072 requests on take more shared memory than a kernel has by default: what one
+    """Batches of thousands of requests take more shared memory than a kernel has by default: what one
     thread's call allows must not be taken from another's."""
     lib = _native.lib()
     codes, states = {}, {}
